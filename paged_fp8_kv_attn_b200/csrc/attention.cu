@@ -584,6 +584,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             Segment sn;
             const bool have_next = walk.next(sn);
             PageWindow next_win;
+            next_win.reset(nullptr);   // (holds no entries: load_meta must load them)
             const int next_aborted = have_next ? load_meta(sn, next_win) : 0;
             if (aborted) {
                 win = next_win;
