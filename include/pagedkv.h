@@ -1,6 +1,6 @@
 /*
- * pagedkv.h -- C ABI of the paged FP8-KV decode library for NVIDIA B200
- * (sm_100a).
+ * pagedkv.h -- C ABI of the paged KV-cache decode library (FP8, BF16 and
+ * 4-bit caches) for NVIDIA B200 (sm_100a).
  *
  * The calls follow the problem as the source pages state it: a pool of
  * physical KV-cache pages; per request a page table (logical page ->
@@ -28,6 +28,16 @@
  *  - KV pools are laid out [num_pages][num_kv_heads][page_size][head_dim],
  *    so one (page, KV head) tile is contiguous.  K and V live in separate
  *    pools of the same shape.
+ *  - An INT4 pool is a pair of arrays: 4-bit codes [num_pages][num_kv_heads]
+ *    [page_size][head_dim / 2] uint8 (dim 2i in bits 0-3 of byte i, dim 2i + 1
+ *    in bits 4-7) and parameters [num_pages][num_kv_heads][page_size]
+ *    [head_dim / 64][2] bf16, a pair (s, m) per group of 64 consecutive dims
+ *    of one token; both 16-byte aligned.  The value is s * code + m: 4.5 bits
+ *    an element.  The library writes, for a group with minimum m (a zero as
+ *    +0) and range r = maximum - m, s = bf16(r / 15) and code = min(15,
+ *    round_half_even((x - m) / s)), 0 where s = 0; r, the differences and the
+ *    quotients are binary32.  A group with a NaN, an infinity or an r beyond
+ *    binary32 gets s = m = NaN and codes 0: it reads back as NaN.
  *  - page_table and expected_tags are [batch][max_pages] (row stride
  *    max_pages); only the first ceil(seq_lens[b] / page_size) entries of a
  *    row are ever read.
@@ -81,6 +91,7 @@ typedef int32_t pkv_status;
 
 #define PKV_KV_FP8 0
 #define PKV_KV_BF16 1
+#define PKV_KV_INT4 2
 
 /* Supported shapes: head_dim in {64, 128}; page_size in {16, 32, 64, 128};
  * num_q_heads a multiple of num_kv_heads with a group of at most 16;
@@ -111,6 +122,19 @@ PKV_API pkv_status kv_tag_check(const uint32_t* page_tags, int32_t num_pages,
                         int32_t max_pages, const int32_t* seq_lens, int32_t batch,
                         int32_t page_size, uint8_t* abort_out, int32_t* num_aborted,
                         void* stream);
+
+/*
+ * kv_tag_check_window -- kv_tag_check for a layer whose attention sees the
+ * last `window` and the first `sinks` tokens of a request (window >= 1,
+ * sinks >= 0): an entry whose page holds hidden tokens only is not read, so
+ * that its page may have been given away.  With window >= the length it is
+ * kv_tag_check.
+ */
+PKV_API pkv_status kv_tag_check_window(const uint32_t* page_tags, int32_t num_pages,
+                               const int32_t* page_table, const uint32_t* expected_tags,
+                               int32_t max_pages, const int32_t* seq_lens, int32_t batch,
+                               int32_t page_size, int32_t window, int32_t sinks,
+                               uint8_t* abort_out, int32_t* num_aborted, void* stream);
 
 /*
  * kv_append_fp8 -- quantise each request's new K/V token to E4M3 and write
@@ -148,6 +172,17 @@ PKV_API pkv_status kv_append_bf16(const uint16_t* k_new, const uint16_t* v_new,
                           const uint8_t* abort, void* stream);
 
 /*
+ * kv_append_int4 -- the same write for an INT4 cache: codes and parameters of
+ * the new token's groups (the format is in the conventions above).
+ */
+PKV_API pkv_status kv_append_int4(const uint16_t* k_new, const uint16_t* v_new,
+                          const int32_t* page_table, int32_t max_pages,
+                          const int32_t* seq_lens, int32_t batch, int32_t num_kv_heads,
+                          int32_t head_dim, int32_t page_size, uint8_t* k_codes,
+                          uint16_t* k_params, uint8_t* v_codes, uint16_t* v_params,
+                          int32_t num_pages, const uint8_t* abort, void* stream);
+
+/*
  * kv_check_append_fp8 -- kv_tag_check followed by kv_append_fp8 (with the
  * abort mask just computed), as one kernel with one CTA per request.
  * [T] "保护共享 KV cache" / [S] "共享 KV 快取的完整性檢查": the check stays a
@@ -175,6 +210,107 @@ PKV_API pkv_status kv_check_append_bf16(const uint32_t* page_tags, int32_t num_p
                                 int32_t num_kv_heads, int32_t head_dim, uint16_t* k_cache,
                                 uint16_t* v_cache, uint8_t* abort_out, int32_t* num_aborted,
                                 void* stream);
+
+/* kv_check_append_int4 -- the same for an INT4 cache (kv_append_int4). */
+PKV_API pkv_status kv_check_append_int4(const uint32_t* page_tags, int32_t num_pages,
+                                const int32_t* page_table, const uint32_t* expected_tags,
+                                int32_t max_pages, const int32_t* seq_lens, int32_t batch,
+                                int32_t page_size, const uint16_t* k_new, const uint16_t* v_new,
+                                int32_t num_kv_heads, int32_t head_dim, uint8_t* k_codes,
+                                uint16_t* k_params, uint8_t* v_codes, uint16_t* v_params,
+                                uint8_t* abort_out, int32_t* num_aborted, void* stream);
+
+/*
+ * kv_write_slots_fp8 / _bf16 / _int4 -- write any number of tokens into the
+ * slots that a slot map names: a prefill chunk, or the new tokens of a decode
+ * batch.  Token i's values go to slot s = slot_map[i], which is position
+ * s % page_size of page s / page_size (what kv_extend_tables writes), with
+ * exactly the rounding of kv_append_*.  A token whose slot is outside [0,
+ * num_pages * page_size), as -1 for the padding of a batch, is skipped, and
+ * its values are not read.  The slots of one call are to be distinct: where
+ * two tokens name the same slot, each byte of its row is one of theirs.
+ * k_new, v_new: num_tokens rows of [num_kv_heads][head_dim] bf16, k_stride and
+ * v_stride elements apart (multiples of 8, at least num_kv_heads * head_dim:
+ * K and V may be parts of one wider row); 16-byte aligned.
+ */
+PKV_API pkv_status kv_write_slots_fp8(const uint16_t* k_new, const uint16_t* v_new,
+                              int64_t k_stride, int64_t v_stride, const int32_t* slot_map,
+                              int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t page_size, float k_scale, float v_scale, uint8_t* k_cache,
+                              uint8_t* v_cache, int32_t num_pages, void* stream);
+PKV_API pkv_status kv_write_slots_bf16(const uint16_t* k_new, const uint16_t* v_new,
+                               int64_t k_stride, int64_t v_stride, const int32_t* slot_map,
+                               int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t page_size, uint16_t* k_cache, uint16_t* v_cache,
+                               int32_t num_pages, void* stream);
+PKV_API pkv_status kv_write_slots_int4(const uint16_t* k_new, const uint16_t* v_new,
+                               int64_t k_stride, int64_t v_stride, const int32_t* slot_map,
+                               int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t page_size, uint8_t* k_codes, uint16_t* k_params,
+                               uint8_t* v_codes, uint16_t* v_params, int32_t num_pages,
+                               void* stream);
+
+/*
+ * kv_read_slots_fp8 / _bf16 / _int4 -- the inverse: the values of the slots
+ * that a slot map names as bf16 (FP8: decode(code) * scale, INT4: s * code + m,
+ * binary32 rounded once to bf16), such as a cached prefix that a prefill
+ * attends to.  A token without a slot reads as zeros; the same slot may be
+ * named several times.  Rows and strides as for kv_write_slots_*.
+ */
+PKV_API pkv_status kv_read_slots_fp8(const int32_t* slot_map, int32_t num_tokens,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                             float k_scale, float v_scale, const uint8_t* k_cache,
+                             const uint8_t* v_cache, int32_t num_pages, uint16_t* k_out,
+                             uint16_t* v_out, int64_t k_stride, int64_t v_stride, void* stream);
+PKV_API pkv_status kv_read_slots_bf16(const int32_t* slot_map, int32_t num_tokens,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                              const uint16_t* k_cache, const uint16_t* v_cache, int32_t num_pages,
+                              uint16_t* k_out, uint16_t* v_out, int64_t k_stride,
+                              int64_t v_stride, void* stream);
+PKV_API pkv_status kv_read_slots_int4(const int32_t* slot_map, int32_t num_tokens,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                              const uint8_t* k_codes, const uint16_t* k_params,
+                              const uint8_t* v_codes, const uint16_t* v_params, int32_t num_pages,
+                              uint16_t* k_out, uint16_t* v_out, int64_t k_stride,
+                              int64_t v_stride, void* stream);
+
+/*
+ * kv_extend_tables -- the page tables, slot map and expected tags of a step,
+ * built on the device: request b grows from old_lens[b] to new_lens[b] tokens
+ * and takes the pages that this needs from a stack of free pages.  With
+ * P = page_size and need_b = ceil(new_lens[b] / P) - ceil(old_lens[b] / P):
+ *  - request b fails (failed[b] = 1, otherwise 0) if old_lens[b] < 0,
+ *    new_lens[b] < old_lens[b] or new_lens[b] > max_pages * P, or if need_b > 0
+ *    and the sum of need_i over all i <= b (those that fail for their lengths
+ *    left out) exceeds *num_free.  The requests in front keep their pages.
+ *  - the served requests take their pages in order from the top of the stack,
+ *    free_pages[*num_free - 1] first; entries ceil(old / P) .. ceil(new / P) - 1
+ *    of their page-table rows name them.  With page_tags and expected_tags (both
+ *    or neither), expected_tags gets each new entry's current tag.  No other
+ *    entry is written.
+ *  - *num_free_out = *num_free less the pages taken; it may be *num_free itself.
+ *    (*num_free is read as at least 0 and at most free_capacity.)
+ *  - cu_tokens[b] = sum over i < b of max(0, new_lens[i] - old_lens[i]) (0 for a
+ *    negative old_lens[i]), b = 0 .. batch, no more than 2^31 - 1: the
+ *    packed position of request b's first new token.
+ *  - slot_map[cu_tokens[b] + i] = page * P + offset of position old_lens[b] + i
+ *    in the extended table, for every packed position below max_tokens; -1 for
+ *    the tokens of a failed request, where the page is outside [0, num_pages),
+ *    and behind the last token.
+ * The caller checks failed (and cu_tokens[batch] <= max_tokens) when it reads
+ * the step's results; pages go back by being pushed onto the stack.
+ * old_lens, new_lens [batch]; free_pages [free_capacity], free_capacity <=
+ * num_pages; page_table and expected_tags [batch][max_pages]; slot_map
+ * [max_tokens]; cu_tokens [batch + 1]; failed [batch] uint8.  Apart from
+ * num_free_out the written arrays may not overlap the others.
+ * page_size is 16, 32, 64 or 128, num_pages * page_size < 2^31.  One kernel.
+ */
+PKV_API pkv_status kv_extend_tables(const int32_t* old_lens, const int32_t* new_lens, int32_t batch,
+                            int32_t page_size, const int32_t* free_pages, int32_t free_capacity,
+                            const int32_t* num_free, int32_t* num_free_out, int32_t num_pages,
+                            int32_t* page_table, int32_t max_pages, const uint32_t* page_tags,
+                            uint32_t* expected_tags, int32_t* slot_map, int32_t max_tokens,
+                            int32_t* cu_tokens, uint8_t* failed, void* stream);
 
 /*
  * kv_retag_pages -- device-side tag bump for reallocated pages.
@@ -219,9 +355,23 @@ PKV_API pkv_status kv_requant_pages_fp8(const uint16_t* src_pool, int32_t src_nu
                                 int32_t head_dim, float scale, void* stream);
 
 /*
+ * kv_requant_pages_int4 -- the BF16 -> INT4 page handoff: page src_pages[i] of
+ * the BF16 pool into page dst_pages[i] of the INT4 pool, group by group as
+ * kv_append_int4 writes a token.  dst_codes [dst_num_pages][Hkv][P][D/2],
+ * dst_params [dst_num_pages][Hkv][P][D/64][2]; the rest as for
+ * kv_requant_pages_fp8.
+ */
+PKV_API pkv_status kv_requant_pages_int4(const uint16_t* src_pool, int32_t src_num_pages,
+                                 const int32_t* src_pages, uint8_t* dst_codes,
+                                 uint16_t* dst_params, int32_t dst_num_pages,
+                                 const int32_t* dst_pages, int32_t num_pairs,
+                                 int32_t num_kv_heads, int32_t page_size, int32_t head_dim,
+                                 void* stream);
+
+/*
  * paged_decode_attn_workspace_size -- bytes of device workspace the
- * attention calls need for these sizes.  kv_dtype is PKV_KV_FP8 or
- * PKV_KV_BF16; num_ctas is the value passed to the attention call (0 = the
+ * attention calls need for these sizes, with or without a window.  kv_dtype
+ * is PKV_KV_FP8, PKV_KV_BF16 or PKV_KV_INT4; num_ctas is the value passed to the attention call (0 = the
  * default; > 0 a split-K grid of that many CTAs; -C, C in 1..16, cluster
  * mode, which needs no more than the default).  Returns 0 on invalid
  * arguments (see pkv_last_error).  The
@@ -237,8 +387,8 @@ PKV_API size_t paged_decode_attn_workspace_size(int32_t kv_dtype, int32_t batch,
 
 /*
  * paged_decode_attn_plan -- the work split that paged_decode_attn_fp8
- * (kv_dtype PKV_KV_FP8) or paged_decode_attn_bf16 (PKV_KV_BF16) chooses for
- * these sizes and this num_ctas on the current device, without launching
+ * (kv_dtype PKV_KV_FP8), paged_decode_attn_bf16 (PKV_KV_BF16) or
+ * paged_decode_attn_int4 (PKV_KV_INT4) chooses for these sizes and this num_ctas on the current device, without launching
  * anything: *cluster_size = 0 for split-K (a partial kernel and a merge
  * kernel), C > 0 for cluster mode (one kernel of clusters of C CTAs);
  * *ctas = CTAs of the partial kernel; *launches = kernels one call launches
@@ -381,6 +531,67 @@ PKV_API pkv_status paged_decode_attn_bf16(const uint16_t* q, const uint16_t* k_c
                                   const uint8_t* abort, uint16_t* out, float* lse,
                                   void* workspace, size_t workspace_bytes, int32_t num_ctas,
                                   void* stream);
+
+/*
+ * paged_decode_attn_int4 -- the same attention over an INT4 cache, whose
+ * values s * code + m are formed while they are read (the K product and the V
+ * product run over the codes; scales and minima are applied to scores and
+ * weights).  k_codes / k_params and v_codes / v_params as in the conventions
+ * above; everything else as for paged_decode_attn_fp8.  Workspace from
+ * paged_decode_attn_workspace_size(PKV_KV_INT4, ...).
+ */
+PKV_API pkv_status paged_decode_attn_int4(const uint16_t* q, const uint8_t* k_codes,
+                                  const uint16_t* k_params, const uint8_t* v_codes,
+                                  const uint16_t* v_params, const int32_t* page_table,
+                                  int32_t max_pages, const int32_t* seq_lens, int32_t batch,
+                                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                  int32_t page_size, int32_t num_pages, float sm_scale,
+                                  const uint8_t* abort, uint16_t* out, float* lse,
+                                  void* workspace, size_t workspace_bytes, int32_t num_ctas,
+                                  void* stream);
+
+/*
+ * paged_decode_attn_fp8_window / _bf16_window / _int4_window -- the same
+ * attention with a sliding window and sinks: of a request of L tokens, token t
+ * is visible if t >= L - window or t < sinks (window >= 1, sinks >= 0).  The
+ * sums of paged_decode_attn_fp8 run over the visible tokens; lse is theirs.
+ * Hidden tokens are not attended to and their values do not matter; of the
+ * page-table row only entries that hold a visible token are used, so a hidden
+ * page may have been given away (its id is ignored, valid or not).  A window
+ * of at least max_pages * page_size hides nothing and runs the call without
+ * one.  Lengths, aborted requests, num_ctas and the workspace as for the calls
+ * without a window; the work split depends on window and sinks too
+ * (paged_decode_attn_plan describes the calls without one).
+ */
+PKV_API pkv_status paged_decode_attn_fp8_window(const uint16_t* q, const uint8_t* k_cache,
+                                        const uint8_t* v_cache, float k_scale, float v_scale,
+                                        const int32_t* page_table, int32_t max_pages,
+                                        const int32_t* seq_lens, int32_t batch,
+                                        int32_t num_q_heads, int32_t num_kv_heads,
+                                        int32_t head_dim, int32_t page_size, int32_t num_pages,
+                                        float sm_scale, int32_t window, int32_t sinks,
+                                        const uint8_t* abort, uint16_t* out, float* lse,
+                                        void* workspace, size_t workspace_bytes, int32_t num_ctas,
+                                        void* stream);
+PKV_API pkv_status paged_decode_attn_bf16_window(const uint16_t* q, const uint16_t* k_cache,
+                                         const uint16_t* v_cache, const int32_t* page_table,
+                                         int32_t max_pages, const int32_t* seq_lens, int32_t batch,
+                                         int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t page_size, int32_t num_pages,
+                                         float sm_scale, int32_t window, int32_t sinks,
+                                         const uint8_t* abort, uint16_t* out, float* lse,
+                                         void* workspace, size_t workspace_bytes, int32_t num_ctas,
+                                         void* stream);
+PKV_API pkv_status paged_decode_attn_int4_window(const uint16_t* q, const uint8_t* k_codes,
+                                         const uint16_t* k_params, const uint8_t* v_codes,
+                                         const uint16_t* v_params, const int32_t* page_table,
+                                         int32_t max_pages, const int32_t* seq_lens, int32_t batch,
+                                         int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t page_size, int32_t num_pages,
+                                         float sm_scale, int32_t window, int32_t sinks,
+                                         const uint8_t* abort, uint16_t* out, float* lse,
+                                         void* workspace, size_t workspace_bytes, int32_t num_ctas,
+                                         void* stream);
 
 /*
  * paged_decode_attn_fp8_noalloc -- paged_decode_attn_fp8 for callers that

@@ -17,6 +17,19 @@ Tensors (all on one CUDA device, contiguous):
   expected     [B][MP]         same dtype as page_tags
   abort        [B]             torch.uint8
 
+INT4 caches are pairs of tensors, K and V each:
+  codes        [NP][Hkv][P][D/2]      torch.uint8 (two 4-bit codes per byte)
+  params       [NP][Hkv][P][D/64][2]  torch.bfloat16 (scale, minimum of 64 dims)
+
+Page tables and slots (kv_extend_tables, kv_write_slots_*, kv_read_slots_*):
+  old/new_lens [B]             torch.int32
+  free_pages   [<= NP]         torch.int32   (a stack; top at num_free - 1)
+  num_free     [1]             torch.int32
+  slot_map     [T]             torch.int32   (page * P + offset, or -1)
+  cu_tokens    [B + 1]         torch.int32
+  failed       [B]             torch.uint8
+  token rows   [T][Hkv][D]     torch.bfloat16 (rows may be part of wider ones)
+
 INT4 weight dequantisation GEMV (int4_dequant_gemv):
   x            [B][k]                      torch.bfloat16
   w_tiles      [n/128][k/256][128][128]    torch.uint8 (two signed 4-bit codes per byte)
@@ -36,6 +49,8 @@ LIB_PATH = os.path.join(_HERE, "libpagedkv.so")
 PKV_OK = 0
 PKV_KV_FP8 = 0
 PKV_KV_BF16 = 1
+PKV_KV_INT4 = 2
+INT4_GROUP = 64   # dims that share a (scale, minimum) pair of an INT4 cache
 _STATUS = {1: "invalid argument", 2: "workspace", 3: "unsupported", 4: "CUDA error"}
 
 
@@ -58,6 +73,10 @@ def _load():
                               "`python -m paged_fp8_kv_attn_b200.build`")
         lib = ctypes.CDLL(LIB_PATH)
         P, i32, f32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+        i64 = ctypes.c_int64
+        attn = [P, i32, P, i32, i32, i32, i32, i32, i32, f32]   # page_table .. sm_scale
+        attn_out = [P, P, P, P, sz, i32, P]                     # abort .. stream
+        slots = [P, i32, i32, i32, i32]                         # slot_map .. page_size
         sig = {
             "kv_tag_check": [P, i32, P, P, i32, P, i32, i32, P, P, P],
             "kv_append_fp8": [P, P, P, i32, P, i32, i32, i32, i32, f32, f32, P, P, i32, P, P],
@@ -75,6 +94,22 @@ def _load():
                                        P, P, P, sz, i32, P],
             "paged_decode_attn_fp8_prefix": [P, P, P, f32, f32, P, i32, P, i32, i32, i32, i32, i32,
                                              i32, f32, P, P, P, P, sz, i32, P, P],
+            "kv_tag_check_window": [P, i32, P, P, i32, P, i32, i32, i32, i32, P, P, P],
+            "kv_append_int4": [P, P, P, i32, P, i32, i32, i32, i32, P, P, P, P, i32, P, P],
+            "kv_check_append_int4": [P, i32, P, P, i32, P, i32, i32, P, P, i32, i32, P, P, P, P, P,
+                                     P, P],
+            "kv_requant_pages_int4": [P, i32, P, P, P, i32, P, i32, i32, i32, i32, P],
+            "kv_write_slots_fp8": [P, P, i64, i64, *slots, f32, f32, P, P, i32, P],
+            "kv_write_slots_bf16": [P, P, i64, i64, *slots, P, P, i32, P],
+            "kv_write_slots_int4": [P, P, i64, i64, *slots, P, P, P, P, i32, P],
+            "kv_read_slots_fp8": [*slots, f32, f32, P, P, i32, P, P, i64, i64, P],
+            "kv_read_slots_bf16": [*slots, P, P, i32, P, P, i64, i64, P],
+            "kv_read_slots_int4": [*slots, P, P, P, P, i32, P, P, i64, i64, P],
+            "kv_extend_tables": [P, P, i32, i32, P, i32, P, P, i32, P, i32, P, P, P, i32, P, P, P],
+            "paged_decode_attn_int4": [P, P, P, P, P, *attn, *attn_out],
+            "paged_decode_attn_fp8_window": [P, P, P, f32, f32, *attn, i32, i32, *attn_out],
+            "paged_decode_attn_bf16_window": [P, P, P, *attn, i32, i32, *attn_out],
+            "paged_decode_attn_int4_window": [P, P, P, P, P, *attn, i32, i32, *attn_out],
             "int4_dequant_gemv": [P, P, P, i32, i32, i32, i32, P, P, P],
         }
         for name, args in sig.items():
@@ -137,6 +172,38 @@ def _need(t, dtype, ndim, name):
     return t
 
 
+def _match(name, t, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _here(stream, *tensors):
+    """The call runs on the current device: refuses tensors of another one."""
+    dev = torch.cuda.current_device() if stream is None else stream.device_index
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be on the call's device {dev}, got {t.device}")
+
+
+def _int4_pools(k_codes, k_params, v_codes, v_params):
+    """(NP, Hkv, P, D) of an INT4 cache."""
+    _need(k_codes, torch.uint8, 4, "k_codes")
+    NP, Hkv, P, half = k_codes.shape
+    D = 2 * half
+    _match("v_codes", _need(v_codes, torch.uint8, 4, "v_codes"), k_codes.shape)
+    par = (NP, Hkv, P, D // INT4_GROUP, 2)
+    _match("k_params", _need(k_params, torch.bfloat16, 5, "k_params"), par)
+    _match("v_params", _need(v_params, torch.bfloat16, 5, "v_params"), par)
+    return NP, Hkv, P, D
+
+
+def _pools(k_cache, v_cache, dtype):
+    """(NP, Hkv, P, D) of an FP8 or BF16 cache."""
+    _need(k_cache, dtype, 4, "k_cache")
+    _match("v_cache", _need(v_cache, dtype, 4, "v_cache"), k_cache.shape)
+    return tuple(k_cache.shape)
+
+
 _TAG_DTYPES = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
 
 
@@ -154,6 +221,28 @@ def kv_tag_check(page_tags, page_table, expected_tags, seq_lens, page_size, abor
     _check("kv_tag_check", _load().kv_tag_check(
         _ptr(page_tags), page_tags.shape[0], _ptr(page_table), _ptr(expected_tags), MP,
         _ptr(seq_lens), B, page_size, _ptr(abort_out), _ptr(num_aborted), _stream(stream)))
+
+
+def kv_tag_check_window(page_tags, page_table, expected_tags, seq_lens, page_size, window, sinks,
+                        abort_out, num_aborted=None, stream=None):
+    """kv_tag_check of the pages that hold one of the last `window` or the first
+    `sinks` tokens of a request; entries of hidden pages are not read."""
+    _need(page_tags, _TAG_DTYPES, 1, "page_tags")
+    _need(page_table, torch.int32, 2, "page_table")
+    _need(expected_tags, _TAG_DTYPES, 2, "expected_tags")
+    _need(seq_lens, torch.int32, 1, "seq_lens")
+    _need(abort_out, torch.uint8, 1, "abort_out")
+    B, MP = page_table.shape
+    _match("expected_tags", expected_tags, (B, MP))
+    _match("seq_lens", seq_lens, (B,))
+    _match("abort_out", abort_out, (B,))
+    if num_aborted is not None:
+        _need(num_aborted, torch.int32, 1, "num_aborted")
+    _here(stream, page_tags, page_table, expected_tags, seq_lens, abort_out, num_aborted)
+    _check("kv_tag_check_window", _load().kv_tag_check_window(
+        _ptr(page_tags), page_tags.shape[0], _ptr(page_table), _ptr(expected_tags), MP,
+        _ptr(seq_lens), B, page_size, int(window), int(sinks), _ptr(abort_out), _ptr(num_aborted),
+        _stream(stream)))
 
 
 def kv_retag_pages(page_tags, pages, stream=None):
@@ -258,6 +347,148 @@ def kv_check_append_bf16(page_tags, page_table, expected_tags, seq_lens, page_si
         _ptr(v_cache), _ptr(abort_out), _ptr(num_aborted), _stream(stream)))
 
 
+def kv_append_int4(k_new, v_new, page_table, seq_lens, page_size, k_codes, k_params, v_codes,
+                   v_params, abort=None, stream=None):
+    """Quantise each request's new K/V token to 4 bits and write it into its page."""
+    NP, Hkv, P, D = _int4_pools(k_codes, k_params, v_codes, v_params)
+    B = _new_tokens(k_new, v_new, page_table, seq_lens, Hkv, P, D, page_size)
+    if abort is not None:
+        _match("abort", _need(abort, torch.uint8, 1, "abort"), (B,))
+    _here(stream, k_new, v_new, page_table, seq_lens, k_codes, k_params, v_codes, v_params, abort)
+    _check("kv_append_int4", _load().kv_append_int4(
+        _ptr(k_new), _ptr(v_new), _ptr(page_table), page_table.shape[1], _ptr(seq_lens), B, Hkv,
+        D, page_size, _ptr(k_codes), _ptr(k_params), _ptr(v_codes), _ptr(v_params), NP,
+        _ptr(abort), _stream(stream)))
+
+
+def kv_check_append_int4(page_tags, page_table, expected_tags, seq_lens, page_size, k_new, v_new,
+                         k_codes, k_params, v_codes, v_params, abort_out, num_aborted=None,
+                         stream=None):
+    """kv_tag_check then kv_append_int4 (with that abort mask) in one kernel."""
+    NP, Hkv, P, D = _int4_pools(k_codes, k_params, v_codes, v_params)
+    B = _new_tokens(k_new, v_new, page_table, seq_lens, Hkv, P, D, page_size)
+    _match("page_tags", _need(page_tags, _TAG_DTYPES, 1, "page_tags"), (NP,))
+    _match("expected_tags", _need(expected_tags, _TAG_DTYPES, 2, "expected_tags"), page_table.shape)
+    _match("abort_out", _need(abort_out, torch.uint8, 1, "abort_out"), (B,))
+    if num_aborted is not None:
+        _need(num_aborted, torch.int32, 1, "num_aborted")
+    _here(stream, page_tags, expected_tags, k_new, v_new, page_table, seq_lens, k_codes, k_params,
+          v_codes, v_params, abort_out, num_aborted)
+    _check("kv_check_append_int4", _load().kv_check_append_int4(
+        _ptr(page_tags), NP, _ptr(page_table), _ptr(expected_tags), page_table.shape[1],
+        _ptr(seq_lens), B, page_size, _ptr(k_new), _ptr(v_new), Hkv, D, _ptr(k_codes),
+        _ptr(k_params), _ptr(v_codes), _ptr(v_params), _ptr(abort_out), _ptr(num_aborted),
+        _stream(stream)))
+
+
+def _new_tokens(k_new, v_new, page_table, seq_lens, Hkv, P, D, page_size):
+    """The batch of an append to a cache of [Hkv][P][D] pages."""
+    _need(k_new, torch.bfloat16, 3, "k_new")
+    _need(page_table, torch.int32, 2, "page_table")
+    B = page_table.shape[0]
+    _match("k_new", k_new, (B, Hkv, D))
+    _match("v_new", _need(v_new, torch.bfloat16, 3, "v_new"), (B, Hkv, D))
+    _match("seq_lens", _need(seq_lens, torch.int32, 1, "seq_lens"), (B,))
+    if page_size != P:
+        raise ValueError(f"page_size is {page_size}, the cache's pages hold {P} tokens")
+    return B
+
+
+def _token_rows(t, name, T, Hkv, D):
+    """Row stride of [T][Hkv][D] token rows, each row contiguous."""
+    if t is None or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
+    _match(name, t, (T, Hkv, D))
+    if T == 0:
+        return Hkv * D
+    if t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != D) or (T > 1 and t.stride(0) < Hkv * D):
+        raise ValueError(f"{name} must hold each token's [Hkv][D] values contiguously")
+    return t.stride(0) if T > 1 else Hkv * D
+
+
+def _slot_call(name, slot_map, pools, scales, k, v, shape, write, stream):
+    _need(slot_map, torch.int32, 1, "slot_map")
+    T = slot_map.shape[0]
+    NP, Hkv, P, D = shape
+    ks, vs = _token_rows(k, "k", T, Hkv, D), _token_rows(v, "v", T, Hkv, D)
+    _here(stream, slot_map, *pools, k, v)
+    mid = (_ptr(slot_map), T, Hkv, D, P, *scales, *map(_ptr, pools), NP)
+    rows, strides = (_ptr(k), _ptr(v)), (ks, vs)
+    args = (*rows, *strides, *mid) if write else (*mid, *rows, *strides)
+    _check(name, getattr(_load(), name)(*args, _stream(stream)))
+
+
+def kv_write_slots_fp8(k_new, v_new, slot_map, k_scale, v_scale, k_cache, v_cache, stream=None):
+    """Quantise token rows to E4M3 and write row i into slot slot_map[i] (negative: skipped)."""
+    _slot_call("kv_write_slots_fp8", slot_map, (k_cache, v_cache), (float(k_scale), float(v_scale)),
+               k_new, v_new, _pools(k_cache, v_cache, torch.uint8), True, stream)
+
+
+def kv_write_slots_bf16(k_new, v_new, slot_map, k_cache, v_cache, stream=None):
+    """Write token row i into slot slot_map[i] of a BF16 cache (negative: skipped)."""
+    _slot_call("kv_write_slots_bf16", slot_map, (k_cache, v_cache), (), k_new, v_new,
+               _pools(k_cache, v_cache, torch.bfloat16), True, stream)
+
+
+def kv_write_slots_int4(k_new, v_new, slot_map, k_codes, k_params, v_codes, v_params, stream=None):
+    """Quantise token rows to 4 bits and write row i into slot slot_map[i] (negative: skipped)."""
+    pools = (k_codes, k_params, v_codes, v_params)
+    _slot_call("kv_write_slots_int4", slot_map, pools, (), k_new, v_new, _int4_pools(*pools), True,
+               stream)
+
+
+def kv_read_slots_fp8(slot_map, k_scale, v_scale, k_cache, v_cache, k_out, v_out, stream=None):
+    """The bf16 values of the slots that slot_map names (zeros for none) of an E4M3 cache."""
+    _slot_call("kv_read_slots_fp8", slot_map, (k_cache, v_cache), (float(k_scale), float(v_scale)),
+               k_out, v_out, _pools(k_cache, v_cache, torch.uint8), False, stream)
+
+
+def kv_read_slots_bf16(slot_map, k_cache, v_cache, k_out, v_out, stream=None):
+    """The values of the slots that slot_map names (zeros for none) of a BF16 cache."""
+    _slot_call("kv_read_slots_bf16", slot_map, (k_cache, v_cache), (), k_out, v_out,
+               _pools(k_cache, v_cache, torch.bfloat16), False, stream)
+
+
+def kv_read_slots_int4(slot_map, k_codes, k_params, v_codes, v_params, k_out, v_out, stream=None):
+    """The bf16 values of the slots that slot_map names (zeros for none) of an INT4 cache."""
+    pools = (k_codes, k_params, v_codes, v_params)
+    _slot_call("kv_read_slots_int4", slot_map, pools, (), k_out, v_out, _int4_pools(*pools), False,
+               stream)
+
+
+def kv_extend_tables(old_lens, new_lens, page_size, free_pages, num_free, page_table, slot_map,
+                     cu_tokens, failed, num_free_out, num_pages, page_tags=None,
+                     expected_tags=None, stream=None):
+    """Grow each request from old_lens[b] to new_lens[b] tokens: take pages from the
+    free stack into page_table (and their tags into expected_tags), and write the new
+    tokens' slots, their packed offsets cu_tokens, the failed flags and num_free_out
+    (which may be num_free)."""
+    for name, t in (("old_lens", old_lens), ("new_lens", new_lens), ("free_pages", free_pages),
+                    ("num_free", num_free), ("slot_map", slot_map), ("cu_tokens", cu_tokens),
+                    ("num_free_out", num_free_out)):
+        _need(t, torch.int32, 1, name)
+    B, MP = _need(page_table, torch.int32, 2, "page_table").shape
+    _need(failed, torch.uint8, 1, "failed")
+    for name, t, n in (("old_lens", old_lens, B), ("new_lens", new_lens, B), ("failed", failed, B),
+                       ("cu_tokens", cu_tokens, B + 1), ("num_free", num_free, 1),
+                       ("num_free_out", num_free_out, 1)):
+        _match(name, t, (n,))
+    if (page_tags is None) != (expected_tags is None):
+        raise ValueError("page_tags and expected_tags are given together or not at all")
+    if page_tags is not None:
+        _match("page_tags", _need(page_tags, _TAG_DTYPES, 1, "page_tags"), (num_pages,))
+        _match("expected_tags", _need(expected_tags, _TAG_DTYPES, 2, "expected_tags"), (B, MP))
+    _here(stream, old_lens, new_lens, free_pages, num_free, num_free_out, page_table, page_tags,
+          expected_tags, slot_map, cu_tokens, failed)
+    _check("kv_extend_tables", _load().kv_extend_tables(
+        _ptr(old_lens), _ptr(new_lens), B, int(page_size), _ptr(free_pages), free_pages.shape[0],
+        _ptr(num_free), _ptr(num_free_out), int(num_pages), _ptr(page_table), MP, _ptr(page_tags),
+        _ptr(expected_tags), _ptr(slot_map), slot_map.shape[0], _ptr(cu_tokens), _ptr(failed),
+        _stream(stream)))
+
+
 def kv_requant_pages_fp8(src_pool, src_pages, dst_pool, dst_pages, scale, stream=None):
     """BF16 -> FP8 page handoff: page src_pages[i] -> dst_pages[i]."""
     _need(src_pool, torch.bfloat16, 4, "src_pool")
@@ -272,6 +503,21 @@ def kv_requant_pages_fp8(src_pool, src_pages, dst_pool, dst_pages, scale, stream
     _check("kv_requant_pages_fp8", _load().kv_requant_pages_fp8(
         _ptr(src_pool), NPs, _ptr(src_pages), _ptr(dst_pool), dst_pool.shape[0], _ptr(dst_pages),
         src_pages.shape[0], Hkv, P, D, float(scale), _stream(stream)))
+
+
+def kv_requant_pages_int4(src_pool, src_pages, dst_codes, dst_params, dst_pages, stream=None):
+    """BF16 -> INT4 page handoff: page src_pages[i] -> dst_pages[i]."""
+    NPs, Hkv, P, D = _need(src_pool, torch.bfloat16, 4, "src_pool").shape
+    _need(src_pages, torch.int32, 1, "src_pages")
+    _match("dst_pages", _need(dst_pages, torch.int32, 1, "dst_pages"), src_pages.shape)
+    NPd = _need(dst_codes, torch.uint8, 4, "dst_codes").shape[0]
+    _match("dst_codes", dst_codes, (NPd, Hkv, P, D // 2))
+    _match("dst_params", _need(dst_params, torch.bfloat16, 5, "dst_params"),
+           (NPd, Hkv, P, D // INT4_GROUP, 2))
+    _here(stream, src_pool, src_pages, dst_codes, dst_params, dst_pages)
+    _check("kv_requant_pages_int4", _load().kv_requant_pages_int4(
+        _ptr(src_pool), NPs, _ptr(src_pages), _ptr(dst_codes), _ptr(dst_params), NPd,
+        _ptr(dst_pages), src_pages.shape[0], Hkv, P, D, _stream(stream)))
 
 
 def paged_decode_attn_workspace_size(kv_dtype, batch, num_q_heads, num_kv_heads, head_dim,
@@ -388,6 +634,65 @@ def paged_decode_attn_bf16(q, k_cache, v_cache, page_table, seq_lens, sm_scale, 
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), page_table.shape[1],
         _ptr(seq_lens), B, Hq, Hkv, D, P, NP, float(sm_scale), _ptr(abort), _ptr(out), _ptr(lse),
         _ptr(workspace), workspace.numel(), num_ctas, _stream(stream)))
+
+
+def _attn_call(name, pools, scales, shape, q, page_table, seq_lens, sm_scale, window, out, lse, workspace,
+               abort, num_ctas, stream):
+    """One attention call over a cache of `shape` = (NP, Hkv, P, D); pools are its
+    tensors, scales those of FP8 pools, window the (window, sinks) pair or ()."""
+    NP, Hkv, P, D = shape
+    _need(q, torch.bfloat16, 3, "q")
+    B, Hq, Dq = q.shape
+    if Dq != D:
+        raise ValueError("head_dim of q and cache differ")
+    if _need(page_table, torch.int32, 2, "page_table").shape[0] != B:
+        raise ValueError("page_table must have a row per request")
+    _match("seq_lens", _need(seq_lens, torch.int32, 1, "seq_lens"), (B,))
+    _match("out", _need(out, torch.bfloat16, 3, "out"), (B, Hq, D))
+    _match("lse", _need(lse, torch.float32, 2, "lse"), (B, Hq))
+    _need(workspace, torch.uint8, 1, "workspace")
+    if abort is not None:
+        _match("abort", _need(abort, torch.uint8, 1, "abort"), (B,))
+    _here(stream, q, *pools, page_table, seq_lens, out, lse, workspace, abort)
+    _check(name, getattr(_load(), name)(
+        _ptr(q), *map(_ptr, pools), *scales, _ptr(page_table), page_table.shape[1], _ptr(seq_lens), B, Hq, Hkv, D, P,
+        NP, float(sm_scale), *window, _ptr(abort), _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace.numel(), num_ctas, _stream(stream)))
+
+
+def paged_decode_attn_int4(q, k_codes, k_params, v_codes, v_params, page_table, seq_lens, sm_scale,
+                           out, lse, workspace, abort=None, num_ctas=0, stream=None):
+    """Decode attention over a paged INT4 cache; writes out (bf16) and lse (fp32)."""
+    pools = (k_codes, k_params, v_codes, v_params)
+    _attn_call("paged_decode_attn_int4", pools, (), _int4_pools(*pools), q, page_table, seq_lens,
+               sm_scale, (), out, lse, workspace, abort, num_ctas, stream)
+
+
+def paged_decode_attn_fp8_window(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens,
+                                 sm_scale, window, sinks, out, lse, workspace, abort=None,
+                                 num_ctas=0, stream=None):
+    """paged_decode_attn_fp8 over the last `window` and the first `sinks` tokens."""
+    _attn_call("paged_decode_attn_fp8_window", (k_cache, v_cache), (float(k_scale), float(v_scale)),
+               _pools(k_cache, v_cache, torch.uint8), q, page_table, seq_lens, sm_scale,
+               (int(window), int(sinks)), out, lse, workspace, abort, num_ctas, stream)
+
+
+def paged_decode_attn_bf16_window(q, k_cache, v_cache, page_table, seq_lens, sm_scale, window,
+                                  sinks, out, lse, workspace, abort=None, num_ctas=0, stream=None):
+    """paged_decode_attn_bf16 over the last `window` and the first `sinks` tokens."""
+    _attn_call("paged_decode_attn_bf16_window", (k_cache, v_cache), (),
+               _pools(k_cache, v_cache, torch.bfloat16), q, page_table, seq_lens, sm_scale,
+               (int(window), int(sinks)), out, lse, workspace, abort, num_ctas, stream)
+
+
+def paged_decode_attn_int4_window(q, k_codes, k_params, v_codes, v_params, page_table, seq_lens,
+                                  sm_scale, window, sinks, out, lse, workspace, abort=None,
+                                  num_ctas=0, stream=None):
+    """paged_decode_attn_int4 over the last `window` and the first `sinks` tokens."""
+    pools = (k_codes, k_params, v_codes, v_params)
+    _attn_call("paged_decode_attn_int4_window", pools, (), _int4_pools(*pools), q,
+               page_table, seq_lens, sm_scale, (int(window), int(sinks)), out, lse, workspace,
+               abort, num_ctas, stream)
 
 
 def paged_decode_attn_fp8_noalloc(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens,

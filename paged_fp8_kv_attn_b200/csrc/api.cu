@@ -36,6 +36,9 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
+bool known_kv(int32_t kv) {
+    return kv == PKV_KV_FP8 || kv == PKV_KV_BF16 || kv == PKV_KV_INT4;
+}
 bool supported_head_dim(int32_t d) { return d == 64 || d == 128; }
 bool supported_page_size(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128; }
 
@@ -46,9 +49,10 @@ constexpr int kMaxDevices = 64;
 struct DeviceInfo {
     bool ready = false;
     int sms = 0;
-    int occupancy[2][2][2][2] = {};   // [fp8][d128][gp16][two KV heads per item]
+    // [cache type][d128][gp16][two KV heads per item][window]
+    int occupancy[3][2][2][2][2] = {};
     // resident clusters of each size (index = cluster size; -1 = not queried)
-    int clusters[2][2][2][2][pkv::kMaxCluster + 1];
+    int clusters[3][2][2][2][2][pkv::kMaxCluster + 1];
 };
 std::mutex g_dev_mutex;
 DeviceInfo g_dev[kMaxDevices];
@@ -65,21 +69,18 @@ pkv_status device_info(const DeviceInfo** out) {
         if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
         e = pkv::step_kernels_set_carveout();
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-        for (int f = 0; f < 2; ++f)
-            for (int d = 0; d < 2; ++d)
-                for (int gp = 0; gp < 2; ++gp)
-                    for (int h2 = 0; h2 < 2; ++h2) {
-                        const bool fp8 = f == 1;
-                        const int hd = d ? 128 : 64, gpad = gp ? 16 : 8, kvh = h2 ? 2 : 1;
-                        if (pkv::attn_partial_smem_bytes(fp8, hd, gpad, kvh) == 0) continue;
-                        e = pkv::attn_set_smem_attr(fp8, hd, gpad, kvh);
-                        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-                        int blocks = 0;
-                        e = pkv::attn_occupancy(fp8, hd, gpad, kvh, &blocks);
-                        if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
-                        info.occupancy[f][d][gp][h2] = blocks < 1 ? 1 : blocks;
-                        for (int c = 0; c <= pkv::kMaxCluster; ++c) info.clusters[f][d][gp][h2][c] = -1;
-                    }
+        for (int i = 0; i < 3 * 16; ++i) {
+            const int kv = i / 16, d = i & 1, gp = (i >> 1) & 1, h2 = (i >> 2) & 1, w = (i >> 3) & 1;
+            const pkv::AttnVariant v{kv, d ? 128 : 64, gp ? 16 : 8, h2 ? 2 : 1, w == 1};
+            if (pkv::attn_partial_smem_bytes(v) == 0) continue;
+            e = pkv::attn_set_smem_attr(v);
+            if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+            int blocks = 0;
+            e = pkv::attn_occupancy(v, &blocks);
+            if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
+            info.occupancy[kv][d][gp][h2][w] = blocks < 1 ? 1 : blocks;
+            for (int c = 0; c <= pkv::kMaxCluster; ++c) info.clusters[kv][d][gp][h2][w][c] = -1;
+        }
         info.ready = true;
     }
     *out = &info;
@@ -88,19 +89,23 @@ pkv_status device_info(const DeviceInfo** out) {
 
 int group_pad_of(int group) { return group <= 8 ? 8 : 16; }
 
+pkv::AttnVariant variant_of(int kv, int head_dim, int group, int kv_per_item, bool window) {
+    return {kv, head_dim, group_pad_of(group), kv_per_item, window};
+}
+
 // Clusters of `size` CTAs of this attention variant that fit on the device at
 // once (queried once per device, variant and size).
-pkv_status max_clusters(bool fp8, int head_dim, int group, int kv_per_item, int size, int* out) {
+pkv_status max_clusters(const pkv::AttnVariant& v, int size, int* out) {
     const DeviceInfo* cinfo = nullptr;
     pkv_status st = device_info(&cinfo);
     if (st != PKV_OK) return st;
     DeviceInfo& info = const_cast<DeviceInfo&>(*cinfo);
     std::lock_guard<std::mutex> lock(g_dev_mutex);
-    int& slot = info.clusters[fp8 ? 1 : 0][head_dim == 128][group > 8][kv_per_item == 2][size];
+    int& slot = info.clusters[v.kv][v.head_dim == 128][v.group_pad == 16][v.kv_per_item == 2]
+                             [v.window][size];
     if (slot < 0) {
         int n = 0;
-        cudaError_t e = pkv::attn_max_clusters(fp8, head_dim, group_pad_of(group), kv_per_item,
-                                               size, &n);
+        cudaError_t e = pkv::attn_max_clusters(v, size, &n);
         if (e != cudaSuccess) {
             cudaGetLastError();   // a refused shape is an answer, not a sticky error
             n = 0;
@@ -118,8 +123,8 @@ pkv_status max_clusters(bool fp8, int head_dim, int group, int kv_per_item, int 
 // over 2..kMaxCluster.  Among sizes that tie, the largest portable one (at
 // most 8) wins: more CTAs share each cluster's items, which evens out
 // requests of unequal length.  Returns C = 0 when no cluster shape fits.
-pkv_status choose_clusters(bool fp8, int head_dim, int group, int kv_per_item, int64_t items,
-                           int forced, int* size, int* count) {
+pkv_status choose_clusters(const pkv::AttnVariant& v, int64_t items, int forced, int* size,
+                           int* count) {
     *size = 0;
     *count = 0;
     double best = 0.0;
@@ -127,7 +132,7 @@ pkv_status choose_clusters(bool fp8, int head_dim, int group, int kv_per_item, i
     const int c_hi = forced > 0 ? forced : pkv::kMaxCluster;
     for (int c = c_lo; c <= c_hi; ++c) {
         int kmax = 0;
-        pkv_status st = max_clusters(fp8, head_dim, group, kv_per_item, c, &kmax);
+        pkv_status st = max_clusters(v, c, &kmax);
         if (st != PKV_OK) return st;
         if (kmax <= 0) continue;
         const int64_t k = std::min<int64_t>(items, kmax);
@@ -142,11 +147,12 @@ pkv_status choose_clusters(bool fp8, int head_dim, int group, int kv_per_item, i
     return PKV_OK;
 }
 
-pkv_status default_ctas(bool fp8, int head_dim, int group, int kv_per_item, int* ctas) {
+pkv_status default_ctas(const pkv::AttnVariant& v, int* ctas) {
     const DeviceInfo* info = nullptr;
     pkv_status st = device_info(&info);
     if (st != PKV_OK) return st;
-    *ctas = info->sms * info->occupancy[fp8 ? 1 : 0][head_dim == 128][group > 8][kv_per_item == 2];
+    *ctas = info->sms * info->occupancy[v.kv][v.head_dim == 128][v.group_pad == 16]
+                                       [v.kv_per_item == 2][v.window];
     return PKV_OK;
 }
 
@@ -175,20 +181,24 @@ pkv_status get_encoder(EncodeTiledFn* fn) {
     return PKV_OK;
 }
 
-pkv_status encode_pool_map(CUtensorMap* map, const void* pool, bool fp8, int head_dim,
+pkv_status encode_pool_map(CUtensorMap* map, const void* pool, int kv, int head_dim,
                            int64_t rows, int box_rows) {
     EncodeTiledFn encode = nullptr;
     pkv_status st = get_encoder(&encode);
     if (st != PKV_OK) return st;
-    const int esize = fp8 ? 1 : 2;
-    const int box_inner = fp8 ? head_dim : 64;  // elements; 64 or 128 bytes
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(head_dim) * esize};
+    const bool bytes = kv != PKV_KV_BF16;
+    // row elements: codes (FP8), pairs of codes (INT4) or bf16 values
+    const int inner = kv == PKV_KV_INT4 ? head_dim / 2 : head_dim;
+    const int esize = bytes ? 1 : 2;
+    const int box_inner = bytes ? inner : 64;   // elements; 32, 64 or 128 bytes
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner) * esize};
     cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_rows)};
     cuuint32_t estr[2] = {1, 1};
-    const CUtensorMapSwizzle sw =
-        (box_inner * esize == 128) ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-    CUresult r = encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+    const CUtensorMapSwizzle sw = (box_inner * esize == 128)  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : (box_inner * esize == 64) ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                              : CU_TENSOR_MAP_SWIZZLE_NONE;
+    CUresult r = encode(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                         2, const_cast<void*>(pool), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -241,24 +251,32 @@ struct AttnPlan {
     int nclusters;
 };
 
-pkv_status plan_attention(bool fp8, int32_t batch, int32_t num_kv_heads, int32_t group,
-                          int32_t head_dim, int32_t max_pages, int32_t page_size,
-                          int32_t num_ctas, AttnPlan* plan, bool allow_cluster = true) {
+// The most tokens a request can attend to (window > 0: with that window).
+int64_t max_visible(int32_t max_pages, int32_t page_size, int32_t window, int32_t sinks) {
+    const int64_t all = static_cast<int64_t>(max_pages) * page_size;
+    return window > 0 ? std::min<int64_t>(all, static_cast<int64_t>(window) + sinks) : all;
+}
+
+pkv_status plan_attention(int kv, int32_t batch, int32_t num_kv_heads, int32_t group,
+                          int32_t head_dim, int32_t max_pages, int32_t page_size, int32_t window,
+                          int32_t sinks, int32_t num_ctas, AttnPlan* plan,
+                          bool allow_cluster = true) {
     pkv_status st = PKV_OK;
-    int kv_per_item = pkv::kv_heads_per_item(fp8, num_kv_heads, group);
+    int kv_per_item = pkv::kv_heads_per_item(kv, num_kv_heads, group);
     plan->ws_kv_per_item = kv_per_item;
     int grid = num_ctas > 0 ? num_ctas : 0;
     if (grid == 0) {
         // one wave of resident CTAs, but no more than leaves each CTA about
         // eight 64-token chunks of the largest batch the page table allows
         // (small batches gain from fewer, longer segments and a lighter merge)
-        st = default_ctas(fp8, head_dim, group, kv_per_item, &grid);
+        st = default_ctas(variant_of(kv, head_dim, group, kv_per_item, window > 0), &grid);
         if (st != PKV_OK) return st;
         const DeviceInfo* info = nullptr;
         st = device_info(&info);
         if (st != PKV_OK) return st;
         const int64_t chunks_per_seq =
-            (static_cast<int64_t>(max_pages) * page_size + pkv::kChunkTokens - 1) / pkv::kChunkTokens;
+            (max_visible(max_pages, page_size, window, sinks) + pkv::kChunkTokens - 1) /
+            pkv::kChunkTokens;
         const int64_t max_units =
             static_cast<int64_t>(batch) * (num_kv_heads / kv_per_item) * chunks_per_seq;
         const int64_t cap = std::max<int64_t>(info->sms, (max_units + 7) / 8);
@@ -292,7 +310,7 @@ pkv_status plan_attention(bool fp8, int32_t batch, int32_t num_kv_heads, int32_t
                 items *= 2;
             }
         }
-        st = choose_clusters(fp8, head_dim, group, kv_per_item, items,
+        st = choose_clusters(variant_of(kv, head_dim, group, kv_per_item, window > 0), items,
                              num_ctas < 0 ? -num_ctas : 0, &cluster, &nclusters);
         if (st != PKV_OK) return st;
         if (cluster == 0 && num_ctas < 0)
@@ -305,12 +323,27 @@ pkv_status plan_attention(bool fp8, int32_t batch, int32_t num_kv_heads, int32_t
     return PKV_OK;
 }
 
-pkv_status attn_impl(bool fp8, const uint16_t* q, const void* k_cache, const void* v_cache,
-                     float k_scale, float v_scale, const int32_t* page_table, int32_t max_pages,
-                     const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
-                     int32_t num_kv_heads, int32_t head_dim, int32_t page_size, int32_t num_pages,
-                     float sm_scale, const uint8_t* abort, uint16_t* out, float* lse,
+// The K and V pools of one attention call.
+struct KvPools {
+    int kv;                      // PKV_KV_*
+    const void* k;
+    const void* v;
+    float k_scale, v_scale;      // FP8
+    const uint16_t* k_params;    // INT4
+    const uint16_t* v_params;
+};
+
+// window > 0: only the last `window` and the first `sinks` tokens are visible.
+pkv_status attn_impl(const KvPools& pools, const uint16_t* q, const int32_t* page_table,
+                     int32_t max_pages, const int32_t* seq_lens, int32_t batch,
+                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                     int32_t page_size, int32_t num_pages, float sm_scale, int32_t window,
+                     int32_t sinks, const uint8_t* abort, uint16_t* out, float* lse,
                      void* workspace, size_t workspace_bytes, int32_t num_ctas, void* stream) {
+    const int kv = pools.kv;
+    const bool fp8 = kv == PKV_KV_FP8, int4 = kv == PKV_KV_INT4;
+    const void *k_cache = pools.k, *v_cache = pools.v;
+    const float k_scale = pools.k_scale, v_scale = pools.v_scale;
     pkv_status st = check_common_kv(batch, num_kv_heads, head_dim, page_size, num_pages, max_pages);
     if (st != PKV_OK) return st;
     if (num_q_heads < 1 || num_q_heads % num_kv_heads != 0)
@@ -327,17 +360,21 @@ pkv_status attn_impl(bool fp8, const uint16_t* q, const void* k_cache, const voi
         return fail(PKV_ERR_INVALID_ARG, "num_ctas must be >= %d (got %d)", -pkv::kMaxCluster,
                     num_ctas);
     if (batch == 0) return PKV_OK;
-    if (!q || !k_cache || !v_cache || !page_table || !seq_lens || !out || !lse)
+    if (!q || !k_cache || !v_cache || !page_table || !seq_lens || !out || !lse ||
+        (int4 && (!pools.k_params || !pools.v_params)))
         return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 4) ||
-        !aligned(lse, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4))
+        !aligned(lse, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
+        !aligned(pools.k_params, 16) || !aligned(pools.v_params, 16))
         return fail(PKV_ERR_INVALID_ARG, "misaligned pointer (q and caches need 16 bytes)");
+    // a window that covers every length the page table allows hides nothing
+    if (window >= static_cast<int64_t>(max_pages) * page_size) window = sinks = 0;
     if (!workspace || !aligned(workspace, 256))
         return fail(PKV_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
 
     AttnPlan plan;
-    st = plan_attention(fp8, batch, num_kv_heads, group, head_dim, max_pages, page_size, num_ctas,
-                        &plan);
+    st = plan_attention(kv, batch, num_kv_heads, group, head_dim, max_pages, page_size, window,
+                        sinks, num_ctas, &plan);
     if (st != PKV_OK) return st;
     const int kv_per_item = plan.kv_per_item;
     const int grid = plan.grid;
@@ -356,9 +393,9 @@ pkv_status attn_impl(bool fp8, const uint16_t* q, const void* k_cache, const voi
                              : (page_size < pkv::kChunkTokens ? page_size : pkv::kChunkTokens);
     const int64_t rows = static_cast<int64_t>(num_pages) * num_kv_heads * page_size;
     CUtensorMap tk, tv;
-    st = encode_pool_map(&tk, k_cache, fp8, head_dim, rows, box_rows);
+    st = encode_pool_map(&tk, k_cache, kv, head_dim, rows, box_rows);
     if (st != PKV_OK) return st;
-    st = encode_pool_map(&tv, v_cache, fp8, head_dim, rows, box_rows);
+    st = encode_pool_map(&tv, v_cache, kv, head_dim, rows, box_rows);
     if (st != PKV_OK) return st;
 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -387,9 +424,14 @@ pkv_status attn_impl(bool fp8, const uint16_t* q, const void* k_cache, const voi
     a.num_clusters = nclusters;
     a.qk_scale = sm_scale * (fp8 ? k_scale : 1.f) * 1.4426950408889634f;
     a.v_scale = fp8 ? v_scale : 1.f;
+    a.k_params = reinterpret_cast<const uint8_t*>(pools.k_params);
+    a.v_params = reinterpret_cast<const uint8_t*>(pools.v_params);
+    a.window = window;
+    a.sinks = sinks;
 
-    cudaError_t e = pkv::launch_attn_partial(fp8, head_dim, group_pad_of(group), kv_per_item,
-                                             a.num_ctas, as_stream(stream), tk, tv, a);
+    cudaError_t e = pkv::launch_attn_partial(
+        variant_of(kv, head_dim, group, kv_per_item, window > 0), a.num_ctas, as_stream(stream),
+        tk, tv, a);
     if (e != cudaSuccess) return cuda_fail(e, "attention partial launch");
     if (cluster == 0) {
         e = pkv::launch_attn_merge(head_dim, as_stream(stream), a);
@@ -406,7 +448,7 @@ struct PrefixLayout {
 };
 
 bool prefix_supported(int32_t num_kv_heads, int32_t group, int32_t head_dim) {
-    return head_dim == 128 && pkv::kv_heads_per_item(true, num_kv_heads, group) == 2;
+    return head_dim == 128 && pkv::kv_heads_per_item(PKV_KV_FP8, num_kv_heads, group) == 2;
 }
 
 PrefixLayout prefix_layout(size_t base, int32_t batch, int32_t num_kv_heads, int32_t group) {
@@ -447,9 +489,10 @@ pkv_status prefix_impl(const uint16_t* q, const uint8_t* k_cache, const uint8_t*
                     num_ctas);
     if (!prefix_supported(num_kv_heads, group, head_dim)) {
         // no shared-prefix tile for this shape: the plain call, no chunk shared
-        st = attn_impl(true, q, k_cache, v_cache, k_scale, v_scale, page_table, max_pages,
-                       seq_lens, batch, num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
-                       sm_scale, abort, out, lse, workspace, workspace_bytes, num_ctas, stream);
+        st = attn_impl({PKV_KV_FP8, k_cache, v_cache, k_scale, v_scale, nullptr, nullptr}, q,
+                       page_table, max_pages, seq_lens, batch, num_q_heads, num_kv_heads,
+                       head_dim, page_size, num_pages, sm_scale, 0, 0, abort, out, lse, workspace,
+                       workspace_bytes, num_ctas, stream);
         if (st != PKV_OK || chunk_begin_out == nullptr || batch == 0) return st;
         cudaError_t e = cudaMemsetAsync(chunk_begin_out, 0, static_cast<size_t>(batch) * 4,
                                         as_stream(stream));
@@ -470,8 +513,8 @@ pkv_status prefix_impl(const uint16_t* q, const uint8_t* k_cache, const uint8_t*
         return fail(PKV_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
 
     AttnPlan plan;
-    st = plan_attention(true, batch, num_kv_heads, group, head_dim, max_pages, page_size, num_ctas,
-                        &plan, /*allow_cluster=*/false);
+    st = plan_attention(PKV_KV_FP8, batch, num_kv_heads, group, head_dim, max_pages, page_size, 0, 0,
+                        num_ctas, &plan, /*allow_cluster=*/false);
     if (st != PKV_OK) return st;
     const DeviceInfo* info = nullptr;
     st = device_info(&info);
@@ -513,15 +556,15 @@ pkv_status prefix_impl(const uint16_t* q, const uint8_t* k_cache, const uint8_t*
     const int64_t rows = static_cast<int64_t>(num_pages) * num_kv_heads * page_size;
     CUtensorMap tk_p, tv_p, tk, tv;
     // the prefix pass loads one head's 64 rows (or a page of them) per box
-    st = encode_pool_map(&tk_p, k_cache, true, head_dim, rows, box_rows);
+    st = encode_pool_map(&tk_p, k_cache, PKV_KV_FP8, head_dim, rows, box_rows);
     if (st != PKV_OK) return st;
-    st = encode_pool_map(&tv_p, v_cache, true, head_dim, rows, box_rows);
+    st = encode_pool_map(&tv_p, v_cache, PKV_KV_FP8, head_dim, rows, box_rows);
     if (st != PKV_OK) return st;
     // the split-K kernel's boxes (both heads of a 64-token page at once)
     const int box_rows_s = page_size == pkv::kChunkTokens ? 2 * pkv::kChunkTokens : box_rows;
-    st = encode_pool_map(&tk, k_cache, true, head_dim, rows, box_rows_s);
+    st = encode_pool_map(&tk, k_cache, PKV_KV_FP8, head_dim, rows, box_rows_s);
     if (st != PKV_OK) return st;
-    st = encode_pool_map(&tv, v_cache, true, head_dim, rows, box_rows_s);
+    st = encode_pool_map(&tv, v_cache, PKV_KV_FP8, head_dim, rows, box_rows_s);
     if (st != PKV_OK) return st;
 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -595,7 +638,8 @@ pkv_status prefix_impl(const uint16_t* q, const uint8_t* k_cache, const uint8_t*
     a.chunk_begin = pa.chunk_begin;
     a.pfx_ml = pa.pfx_ml;
     a.pfx_o = pa.pfx_o;
-    e = pkv::launch_attn_partial(true, head_dim, group_pad_of(group), 2, plan.grid, s, tk, tv, a);
+    e = pkv::launch_attn_partial(variant_of(PKV_KV_FP8, head_dim, group, 2, false), plan.grid, s, tk,
+                                 tv, a);
     if (e != cudaSuccess) return cuda_fail(e, "attention partial launch");
     e = pkv::launch_attn_merge(head_dim, s, a);
     if (e != cudaSuccess) return cuda_fail(e, "attention merge launch");
@@ -631,10 +675,23 @@ const char* pkv_last_error(void) { return g_last_error.c_str(); }
 
 int32_t pkv_version(void) { return 100; }
 
-pkv_status kv_tag_check(const uint32_t* page_tags, int32_t num_pages, const int32_t* page_table,
-                        const uint32_t* expected_tags, int32_t max_pages, const int32_t* seq_lens,
-                        int32_t batch, int32_t page_size, uint8_t* abort_out,
-                        int32_t* num_aborted, void* stream) {
+static pkv_status check_window(int32_t window, int32_t sinks) {
+    if (window < 1) return fail(PKV_ERR_INVALID_ARG, "window must be >= 1 (got %d)", window);
+    if (sinks < 0) return fail(PKV_ERR_INVALID_ARG, "sinks must be >= 0 (got %d)", sinks);
+    return PKV_OK;
+}
+
+// Per-device set-up (kernel attributes) of the calls that need nothing else of it.
+static pkv_status device_setup() {
+    const DeviceInfo* info = nullptr;
+    return device_info(&info);
+}
+
+static pkv_status tag_check_impl(const uint32_t* page_tags, int32_t num_pages,
+                                 const int32_t* page_table, const uint32_t* expected_tags,
+                                 int32_t max_pages, const int32_t* seq_lens, int32_t batch,
+                                 int32_t page_size, int32_t window, int32_t sinks,
+                                 uint8_t* abort_out, int32_t* num_aborted, void* stream) {
     if (batch < 0) return fail(PKV_ERR_INVALID_ARG, "batch must be >= 0");
     if (num_pages < 1 || max_pages < 1 || page_size < 1)
         return fail(PKV_ERR_INVALID_ARG, "num_pages, max_pages and page_size must be >= 1");
@@ -645,43 +702,85 @@ pkv_status kv_tag_check(const uint32_t* page_tags, int32_t num_pages, const int3
         if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(num_aborted)");
     }
     if (batch == 0) return PKV_OK;
-    {
-        const DeviceInfo* info = nullptr;   // per-device set-up (kernel attributes)
-        const pkv_status ds = device_info(&info);
-        if (ds != PKV_OK) return ds;
-    }
+    const pkv_status ds = device_setup();
+    if (ds != PKV_OK) return ds;
     cudaError_t e = pkv::launch_tag_check(page_tags, num_pages, page_table, expected_tags,
-                                          max_pages, seq_lens, batch, page_size, abort_out,
-                                          num_aborted, as_stream(stream));
+                                          max_pages, seq_lens, batch, page_size, window, sinks,
+                                          abort_out, num_aborted, as_stream(stream));
     if (e != cudaSuccess) return cuda_fail(e, "tag check launch");
     return PKV_OK;
 }
 
-static pkv_status append_impl(bool fp8, const uint16_t* k_new, const uint16_t* v_new,
+pkv_status kv_tag_check(const uint32_t* page_tags, int32_t num_pages, const int32_t* page_table,
+                        const uint32_t* expected_tags, int32_t max_pages, const int32_t* seq_lens,
+                        int32_t batch, int32_t page_size, uint8_t* abort_out,
+                        int32_t* num_aborted, void* stream) {
+    return tag_check_impl(page_tags, num_pages, page_table, expected_tags, max_pages, seq_lens,
+                          batch, page_size, 0, 0, abort_out, num_aborted, stream);
+}
+
+pkv_status kv_tag_check_window(const uint32_t* page_tags, int32_t num_pages,
+                               const int32_t* page_table, const uint32_t* expected_tags,
+                               int32_t max_pages, const int32_t* seq_lens, int32_t batch,
+                               int32_t page_size, int32_t window, int32_t sinks,
+                               uint8_t* abort_out, int32_t* num_aborted, void* stream) {
+    const pkv_status st = check_window(window, sinks);
+    if (st != PKV_OK) return st;
+    return tag_check_impl(page_tags, num_pages, page_table, expected_tags, max_pages, seq_lens,
+                          batch, page_size, window, sinks, abort_out, num_aborted, stream);
+}
+
+// The scales of an FP8 cache, and the pools of any cache (non-null, aligned).
+static pkv_status check_scales(const pkv::KvDst& c) {
+    if (c.kv == PKV_KV_FP8 && (!(c.k_scale > 0.f) || !(c.v_scale > 0.f) ||
+                               !std::isfinite(c.k_scale) || !std::isfinite(c.v_scale)))
+        return fail(PKV_ERR_INVALID_ARG, "k_scale and v_scale must be finite and > 0");
+    return PKV_OK;
+}
+static pkv_status check_pools(const pkv::KvDst& c) {
+    if (!c.k || !c.v || (c.kv == PKV_KV_INT4 && (!c.k_params || !c.v_params)))
+        return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.k_params, 16) ||
+        !aligned(c.v_params, 16))
+        return fail(PKV_ERR_INVALID_ARG, "the caches must be 16-byte aligned");
+    return PKV_OK;
+}
+
+static pkv::KvDst fp8_pools(const uint8_t* k, const uint8_t* v, float k_scale, float v_scale) {
+    return {PKV_KV_FP8, const_cast<uint8_t*>(k), const_cast<uint8_t*>(v), k_scale, v_scale,
+            nullptr, nullptr};
+}
+static pkv::KvDst bf16_pools(const uint16_t* k, const uint16_t* v) {
+    return {PKV_KV_BF16, const_cast<uint16_t*>(k), const_cast<uint16_t*>(v), 1.f, 1.f,
+            nullptr, nullptr};
+}
+static pkv::KvDst int4_pools(const uint8_t* k, const uint16_t* kp, const uint8_t* v,
+                             const uint16_t* vp) {
+    return {PKV_KV_INT4, const_cast<uint8_t*>(k), const_cast<uint8_t*>(v), 1.f, 1.f,
+            reinterpret_cast<uint32_t*>(const_cast<uint16_t*>(kp)),
+            reinterpret_cast<uint32_t*>(const_cast<uint16_t*>(vp))};
+}
+
+static pkv_status append_impl(const pkv::KvDst& dst, const uint16_t* k_new, const uint16_t* v_new,
                               const int32_t* page_table, int32_t max_pages,
                               const int32_t* seq_lens, int32_t batch, int32_t num_kv_heads,
-                              int32_t head_dim, int32_t page_size, float k_scale, float v_scale,
-                              void* k_cache, void* v_cache, int32_t num_pages,
+                              int32_t head_dim, int32_t page_size, int32_t num_pages,
                               const uint8_t* abort, void* stream) {
     pkv_status st = check_common_kv(batch, num_kv_heads, head_dim, page_size, num_pages, max_pages);
+    if (st == PKV_OK) st = check_scales(dst);
     if (st != PKV_OK) return st;
-    if (fp8 && (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) ||
-                !std::isfinite(v_scale)))
-        return fail(PKV_ERR_INVALID_ARG, "k_scale and v_scale must be finite and > 0");
     if (batch == 0) return PKV_OK;
-    if (!k_new || !v_new || !page_table || !seq_lens || !k_cache || !v_cache)
+    if (!k_new || !v_new || !page_table || !seq_lens)
         return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
-    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) ||
-        !aligned(v_cache, 16))
-        return fail(PKV_ERR_INVALID_ARG, "k_new, v_new and the caches must be 16-byte aligned");
-    {
-        const DeviceInfo* info = nullptr;   // per-device set-up (kernel attributes)
-        const pkv_status ds = device_info(&info);
-        if (ds != PKV_OK) return ds;
-    }
-    cudaError_t e = pkv::launch_append(fp8, k_new, v_new, page_table, max_pages, seq_lens, batch,
-                                       num_kv_heads, head_dim, page_size, k_scale, v_scale,
-                                       k_cache, v_cache, num_pages, abort, as_stream(stream));
+    st = check_pools(dst);
+    if (st != PKV_OK) return st;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16))
+        return fail(PKV_ERR_INVALID_ARG, "k_new and v_new must be 16-byte aligned");
+    st = device_setup();
+    if (st != PKV_OK) return st;
+    cudaError_t e = pkv::launch_append(dst, k_new, v_new, page_table, max_pages, seq_lens, batch,
+                                       num_kv_heads, head_dim, page_size, num_pages, abort,
+                                       as_stream(stream));
     if (e != cudaSuccess) return cuda_fail(e, "append launch");
     return PKV_OK;
 }
@@ -691,9 +790,9 @@ pkv_status kv_append_fp8(const uint16_t* k_new, const uint16_t* v_new, const int
                          int32_t num_kv_heads, int32_t head_dim, int32_t page_size, float k_scale,
                          float v_scale, uint8_t* k_cache, uint8_t* v_cache, int32_t num_pages,
                          const uint8_t* abort, void* stream) {
-    return append_impl(true, k_new, v_new, page_table, max_pages, seq_lens, batch, num_kv_heads,
-                       head_dim, page_size, k_scale, v_scale, k_cache, v_cache, num_pages, abort,
-                       stream);
+    return append_impl(fp8_pools(k_cache, v_cache, k_scale, v_scale), k_new, v_new, page_table,
+                       max_pages, seq_lens, batch, num_kv_heads, head_dim, page_size, num_pages,
+                       abort, stream);
 }
 
 pkv_status kv_append_bf16(const uint16_t* k_new, const uint16_t* v_new,
@@ -701,43 +800,49 @@ pkv_status kv_append_bf16(const uint16_t* k_new, const uint16_t* v_new,
                           int32_t batch, int32_t num_kv_heads, int32_t head_dim,
                           int32_t page_size, uint16_t* k_cache, uint16_t* v_cache,
                           int32_t num_pages, const uint8_t* abort, void* stream) {
-    return append_impl(false, k_new, v_new, page_table, max_pages, seq_lens, batch, num_kv_heads,
-                       head_dim, page_size, 1.f, 1.f, k_cache, v_cache, num_pages, abort, stream);
+    return append_impl(bf16_pools(k_cache, v_cache), k_new, v_new, page_table, max_pages,
+                       seq_lens, batch, num_kv_heads, head_dim, page_size, num_pages, abort,
+                       stream);
 }
 
-static pkv_status check_append_impl(bool fp8, const uint32_t* page_tags, int32_t num_pages,
-                                    const int32_t* page_table, const uint32_t* expected_tags,
-                                    int32_t max_pages, const int32_t* seq_lens, int32_t batch,
-                                    int32_t page_size, const uint16_t* k_new,
-                                    const uint16_t* v_new, int32_t num_kv_heads,
-                                    int32_t head_dim, float k_scale, float v_scale, void* k_cache,
-                                    void* v_cache, uint8_t* abort_out, int32_t* num_aborted,
-                                    void* stream) {
+pkv_status kv_append_int4(const uint16_t* k_new, const uint16_t* v_new,
+                          const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                          int32_t batch, int32_t num_kv_heads, int32_t head_dim,
+                          int32_t page_size, uint8_t* k_codes, uint16_t* k_params,
+                          uint8_t* v_codes, uint16_t* v_params, int32_t num_pages,
+                          const uint8_t* abort, void* stream) {
+    return append_impl(int4_pools(k_codes, k_params, v_codes, v_params), k_new, v_new, page_table,
+                       max_pages, seq_lens, batch, num_kv_heads, head_dim, page_size, num_pages,
+                       abort, stream);
+}
+
+static pkv_status check_append_impl(const pkv::KvDst& dst, const uint32_t* page_tags,
+                                    int32_t num_pages, const int32_t* page_table,
+                                    const uint32_t* expected_tags, int32_t max_pages,
+                                    const int32_t* seq_lens, int32_t batch, int32_t page_size,
+                                    const uint16_t* k_new, const uint16_t* v_new,
+                                    int32_t num_kv_heads, int32_t head_dim, uint8_t* abort_out,
+                                    int32_t* num_aborted, void* stream) {
     pkv_status st = check_common_kv(batch, num_kv_heads, head_dim, page_size, num_pages, max_pages);
+    if (st == PKV_OK) st = check_scales(dst);
     if (st != PKV_OK) return st;
-    if (fp8 && (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) ||
-                !std::isfinite(v_scale)))
-        return fail(PKV_ERR_INVALID_ARG, "k_scale and v_scale must be finite and > 0");
     if (num_aborted) {
         cudaError_t e = cudaMemsetAsync(num_aborted, 0, sizeof(int32_t), as_stream(stream));
         if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(num_aborted)");
     }
     if (batch == 0) return PKV_OK;
-    if (!page_tags || !page_table || !expected_tags || !seq_lens || !k_new || !v_new ||
-        !k_cache || !v_cache || !abort_out)
+    if (!page_tags || !page_table || !expected_tags || !seq_lens || !k_new || !v_new || !abort_out)
         return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
-    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) ||
-        !aligned(v_cache, 16))
-        return fail(PKV_ERR_INVALID_ARG, "k_new, v_new and the caches must be 16-byte aligned");
-    {
-        const DeviceInfo* info = nullptr;   // per-device set-up (kernel attributes)
-        const pkv_status ds = device_info(&info);
-        if (ds != PKV_OK) return ds;
-    }
-    cudaError_t e = pkv::launch_check_append(fp8, page_tags, num_pages, page_table, expected_tags,
+    st = check_pools(dst);
+    if (st != PKV_OK) return st;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16))
+        return fail(PKV_ERR_INVALID_ARG, "k_new and v_new must be 16-byte aligned");
+    st = device_setup();
+    if (st != PKV_OK) return st;
+    cudaError_t e = pkv::launch_check_append(dst, page_tags, num_pages, page_table, expected_tags,
                                              max_pages, seq_lens, batch, page_size, k_new, v_new,
-                                             num_kv_heads, head_dim, k_scale, v_scale, k_cache,
-                                             v_cache, abort_out, num_aborted, as_stream(stream));
+                                             num_kv_heads, head_dim, abort_out, num_aborted,
+                                             as_stream(stream));
     if (e != cudaSuccess) return cuda_fail(e, "check+append launch");
     return PKV_OK;
 }
@@ -749,9 +854,9 @@ pkv_status kv_check_append_fp8(const uint32_t* page_tags, int32_t num_pages,
                                int32_t num_kv_heads, int32_t head_dim, float k_scale,
                                float v_scale, uint8_t* k_cache, uint8_t* v_cache,
                                uint8_t* abort_out, int32_t* num_aborted, void* stream) {
-    return check_append_impl(true, page_tags, num_pages, page_table, expected_tags, max_pages,
-                             seq_lens, batch, page_size, k_new, v_new, num_kv_heads, head_dim,
-                             k_scale, v_scale, k_cache, v_cache, abort_out, num_aborted, stream);
+    return check_append_impl(fp8_pools(k_cache, v_cache, k_scale, v_scale), page_tags, num_pages,
+                             page_table, expected_tags, max_pages, seq_lens, batch, page_size,
+                             k_new, v_new, num_kv_heads, head_dim, abort_out, num_aborted, stream);
 }
 
 pkv_status kv_check_append_bf16(const uint32_t* page_tags, int32_t num_pages,
@@ -761,9 +866,141 @@ pkv_status kv_check_append_bf16(const uint32_t* page_tags, int32_t num_pages,
                                 int32_t num_kv_heads, int32_t head_dim, uint16_t* k_cache,
                                 uint16_t* v_cache, uint8_t* abort_out, int32_t* num_aborted,
                                 void* stream) {
-    return check_append_impl(false, page_tags, num_pages, page_table, expected_tags, max_pages,
-                             seq_lens, batch, page_size, k_new, v_new, num_kv_heads, head_dim,
-                             1.f, 1.f, k_cache, v_cache, abort_out, num_aborted, stream);
+    return check_append_impl(bf16_pools(k_cache, v_cache), page_tags, num_pages, page_table,
+                             expected_tags, max_pages, seq_lens, batch, page_size, k_new, v_new,
+                             num_kv_heads, head_dim, abort_out, num_aborted, stream);
+}
+
+pkv_status kv_check_append_int4(const uint32_t* page_tags, int32_t num_pages,
+                                const int32_t* page_table, const uint32_t* expected_tags,
+                                int32_t max_pages, const int32_t* seq_lens, int32_t batch,
+                                int32_t page_size, const uint16_t* k_new, const uint16_t* v_new,
+                                int32_t num_kv_heads, int32_t head_dim, uint8_t* k_codes,
+                                uint16_t* k_params, uint8_t* v_codes, uint16_t* v_params,
+                                uint8_t* abort_out, int32_t* num_aborted, void* stream) {
+    return check_append_impl(int4_pools(k_codes, k_params, v_codes, v_params), page_tags,
+                             num_pages, page_table, expected_tags, max_pages, seq_lens, batch,
+                             page_size, k_new, v_new, num_kv_heads, head_dim, abort_out,
+                             num_aborted, stream);
+}
+
+// One token write (out == false) or read (out == true) by slot map.
+static pkv_status slots_impl(const pkv::KvDst& pools, bool out, const uint16_t* k,
+                             const uint16_t* v, int64_t k_stride, int64_t v_stride,
+                             const int32_t* slot_map, int32_t num_tokens, int32_t num_kv_heads,
+                             int32_t head_dim, int32_t page_size, int32_t num_pages,
+                             void* stream) {
+    pkv_status st = check_common_kv(num_tokens, num_kv_heads, head_dim, page_size, num_pages, 1);
+    if (st == PKV_OK) st = check_scales(pools);
+    if (st != PKV_OK) return st;
+    const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
+    if (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
+        return fail(PKV_ERR_INVALID_ARG,
+                    "token strides must be multiples of 8 and at least num_kv_heads * head_dim");
+    if (num_tokens == 0) return PKV_OK;
+    if (!k || !v || !slot_map) return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
+    st = check_pools(pools);
+    if (st != PKV_OK) return st;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 4))
+        return fail(PKV_ERR_INVALID_ARG, "the token rows must be 16-byte aligned");
+    const pkv::SlotArgs a{slot_map, num_tokens, num_kv_heads, head_dim, page_size, num_pages,
+                          k_stride, v_stride};
+    cudaError_t e = out ? pkv::launch_read_slots(pools, const_cast<uint16_t*>(k),
+                                                 const_cast<uint16_t*>(v), a, as_stream(stream))
+                        : pkv::launch_write_slots(pools, k, v, a, as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, out ? "slot read launch" : "slot write launch");
+    return PKV_OK;
+}
+
+pkv_status kv_write_slots_fp8(const uint16_t* k_new, const uint16_t* v_new, int64_t k_stride,
+                              int64_t v_stride, const int32_t* slot_map, int32_t num_tokens,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                              float k_scale, float v_scale, uint8_t* k_cache, uint8_t* v_cache,
+                              int32_t num_pages, void* stream) {
+    return slots_impl(fp8_pools(k_cache, v_cache, k_scale, v_scale), false, k_new, v_new, k_stride,
+                      v_stride, slot_map, num_tokens, num_kv_heads, head_dim, page_size, num_pages,
+                      stream);
+}
+
+pkv_status kv_write_slots_bf16(const uint16_t* k_new, const uint16_t* v_new, int64_t k_stride,
+                               int64_t v_stride, const int32_t* slot_map, int32_t num_tokens,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                               uint16_t* k_cache, uint16_t* v_cache, int32_t num_pages,
+                               void* stream) {
+    return slots_impl(bf16_pools(k_cache, v_cache), false, k_new, v_new, k_stride, v_stride,
+                      slot_map, num_tokens, num_kv_heads, head_dim, page_size, num_pages, stream);
+}
+
+pkv_status kv_write_slots_int4(const uint16_t* k_new, const uint16_t* v_new, int64_t k_stride,
+                               int64_t v_stride, const int32_t* slot_map, int32_t num_tokens,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                               uint8_t* k_codes, uint16_t* k_params, uint8_t* v_codes,
+                               uint16_t* v_params, int32_t num_pages, void* stream) {
+    return slots_impl(int4_pools(k_codes, k_params, v_codes, v_params), false, k_new, v_new,
+                      k_stride, v_stride, slot_map, num_tokens, num_kv_heads, head_dim, page_size,
+                      num_pages, stream);
+}
+
+pkv_status kv_read_slots_fp8(const int32_t* slot_map, int32_t num_tokens, int32_t num_kv_heads,
+                             int32_t head_dim, int32_t page_size, float k_scale, float v_scale,
+                             const uint8_t* k_cache, const uint8_t* v_cache, int32_t num_pages,
+                             uint16_t* k_out, uint16_t* v_out, int64_t k_stride, int64_t v_stride,
+                             void* stream) {
+    return slots_impl(fp8_pools(k_cache, v_cache, k_scale, v_scale), true, k_out, v_out, k_stride,
+                      v_stride, slot_map, num_tokens, num_kv_heads, head_dim, page_size, num_pages,
+                      stream);
+}
+
+pkv_status kv_read_slots_bf16(const int32_t* slot_map, int32_t num_tokens, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t page_size, const uint16_t* k_cache,
+                              const uint16_t* v_cache, int32_t num_pages, uint16_t* k_out,
+                              uint16_t* v_out, int64_t k_stride, int64_t v_stride, void* stream) {
+    return slots_impl(bf16_pools(k_cache, v_cache), true, k_out, v_out, k_stride, v_stride,
+                      slot_map, num_tokens, num_kv_heads, head_dim, page_size, num_pages, stream);
+}
+
+pkv_status kv_read_slots_int4(const int32_t* slot_map, int32_t num_tokens, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t page_size, const uint8_t* k_codes,
+                              const uint16_t* k_params, const uint8_t* v_codes,
+                              const uint16_t* v_params, int32_t num_pages, uint16_t* k_out,
+                              uint16_t* v_out, int64_t k_stride, int64_t v_stride, void* stream) {
+    return slots_impl(int4_pools(k_codes, k_params, v_codes, v_params), true, k_out, v_out,
+                      k_stride, v_stride, slot_map, num_tokens, num_kv_heads, head_dim, page_size,
+                      num_pages, stream);
+}
+
+pkv_status kv_extend_tables(const int32_t* old_lens, const int32_t* new_lens, int32_t batch,
+                            int32_t page_size, const int32_t* free_pages, int32_t free_capacity,
+                            const int32_t* num_free, int32_t* num_free_out, int32_t num_pages,
+                            int32_t* page_table, int32_t max_pages, const uint32_t* page_tags,
+                            uint32_t* expected_tags, int32_t* slot_map, int32_t max_tokens,
+                            int32_t* cu_tokens, uint8_t* failed, void* stream) {
+    if (batch < 0 || max_tokens < 0 || free_capacity < 0)
+        return fail(PKV_ERR_INVALID_ARG, "batch, max_tokens and free_capacity must be >= 0");
+    if (num_pages < 1 || max_pages < 1)
+        return fail(PKV_ERR_INVALID_ARG, "num_pages and max_pages must be >= 1");
+    if (!supported_page_size(page_size))
+        return fail(PKV_ERR_UNSUPPORTED, "page_size %d not supported (16, 32, 64 or 128)", page_size);
+    if (static_cast<int64_t>(num_pages) * page_size > INT32_MAX)
+        return fail(PKV_ERR_UNSUPPORTED, "num_pages * page_size must be < 2^31");
+    if (free_capacity > num_pages)
+        return fail(PKV_ERR_INVALID_ARG, "free_capacity must be at most num_pages");
+    if ((page_tags == nullptr) != (expected_tags == nullptr))
+        return fail(PKV_ERR_INVALID_ARG, "page_tags and expected_tags are given together or not at all");
+    if (!num_free || !num_free_out || !cu_tokens || (free_capacity > 0 && !free_pages) ||
+        (max_tokens > 0 && !slot_map) ||
+        (batch > 0 && (!old_lens || !new_lens || !page_table || !failed)))
+        return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
+    const void* words[] = {old_lens, new_lens,      free_pages, num_free, num_free_out, page_table,
+                           page_tags, expected_tags, slot_map,   cu_tokens};
+    for (const void* p : words)
+        if (!aligned(p, 4)) return fail(PKV_ERR_INVALID_ARG, "misaligned pointer");
+    const pkv::TableArgs a{old_lens,  new_lens,  free_pages,    num_free,  num_free_out, page_table,
+                           page_tags, expected_tags, cu_tokens, slot_map,  failed,       batch,
+                           page_size, free_capacity, num_pages, max_pages, max_tokens};
+    cudaError_t e = pkv::launch_extend_tables(a, as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "extend tables launch");
+    return PKV_OK;
 }
 
 pkv_status kv_retag_pages(uint32_t* page_tags, int32_t num_pages, const int32_t* pages,
@@ -795,11 +1032,9 @@ pkv_status kv_expected_tags(const uint32_t* page_tags, int32_t num_pages,
     return PKV_OK;
 }
 
-pkv_status kv_requant_pages_fp8(const uint16_t* src_pool, int32_t src_num_pages,
-                                const int32_t* src_pages, uint8_t* dst_pool,
-                                int32_t dst_num_pages, const int32_t* dst_pages,
-                                int32_t num_pairs, int32_t num_kv_heads, int32_t page_size,
-                                int32_t head_dim, float scale, void* stream) {
+// The sizes of a page handoff.
+static pkv_status check_requant(int32_t src_num_pages, int32_t dst_num_pages, int32_t num_pairs,
+                                int32_t num_kv_heads, int32_t page_size, int32_t head_dim) {
     if (num_pairs < 0) return fail(PKV_ERR_INVALID_ARG, "num_pairs must be >= 0");
     if (src_num_pages < 1 || dst_num_pages < 1 || num_kv_heads < 1)
         return fail(PKV_ERR_INVALID_ARG, "pool sizes and num_kv_heads must be >= 1");
@@ -807,6 +1042,17 @@ pkv_status kv_requant_pages_fp8(const uint16_t* src_pool, int32_t src_num_pages,
         return fail(PKV_ERR_UNSUPPORTED, "head_dim %d not supported (64 or 128)", head_dim);
     if (!supported_page_size(page_size))
         return fail(PKV_ERR_UNSUPPORTED, "page_size %d not supported", page_size);
+    return PKV_OK;
+}
+
+pkv_status kv_requant_pages_fp8(const uint16_t* src_pool, int32_t src_num_pages,
+                                const int32_t* src_pages, uint8_t* dst_pool,
+                                int32_t dst_num_pages, const int32_t* dst_pages,
+                                int32_t num_pairs, int32_t num_kv_heads, int32_t page_size,
+                                int32_t head_dim, float scale, void* stream) {
+    const pkv_status st = check_requant(src_num_pages, dst_num_pages, num_pairs, num_kv_heads,
+                                        page_size, head_dim);
+    if (st != PKV_OK) return st;
     if (!(scale > 0.f) || !std::isfinite(scale))
         return fail(PKV_ERR_INVALID_ARG, "scale must be finite and > 0");
     if (num_pairs == 0) return PKV_OK;
@@ -822,12 +1068,35 @@ pkv_status kv_requant_pages_fp8(const uint16_t* src_pool, int32_t src_num_pages,
     return PKV_OK;
 }
 
+pkv_status kv_requant_pages_int4(const uint16_t* src_pool, int32_t src_num_pages,
+                                 const int32_t* src_pages, uint8_t* dst_codes,
+                                 uint16_t* dst_params, int32_t dst_num_pages,
+                                 const int32_t* dst_pages, int32_t num_pairs,
+                                 int32_t num_kv_heads, int32_t page_size, int32_t head_dim,
+                                 void* stream) {
+    const pkv_status st = check_requant(src_num_pages, dst_num_pages, num_pairs, num_kv_heads,
+                                        page_size, head_dim);
+    if (st != PKV_OK) return st;
+    if (num_pairs == 0) return PKV_OK;
+    if (!src_pool || !src_pages || !dst_codes || !dst_params || !dst_pages)
+        return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(src_pool, 16) || !aligned(dst_codes, 16) || !aligned(dst_params, 16))
+        return fail(PKV_ERR_INVALID_ARG, "pools must be 16-byte aligned");
+    const int64_t page_elems = static_cast<int64_t>(num_kv_heads) * page_size * head_dim;
+    cudaError_t e = pkv::launch_requant_int4(src_pool, src_num_pages, src_pages, dst_codes,
+                                             reinterpret_cast<uint32_t*>(dst_params),
+                                             dst_num_pages, dst_pages, num_pairs, page_elems,
+                                             head_dim, as_stream(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "requant launch");
+    return PKV_OK;
+}
+
 pkv_status paged_decode_attn_plan(int32_t kv_dtype, int32_t batch, int32_t num_q_heads,
                                   int32_t num_kv_heads, int32_t head_dim, int32_t max_pages,
                                   int32_t page_size, int32_t num_ctas, int32_t* cluster_size,
                                   int32_t* ctas, int32_t* launches) {
-    if (kv_dtype != PKV_KV_FP8 && kv_dtype != PKV_KV_BF16)
-        return fail(PKV_ERR_INVALID_ARG, "kv_dtype must be PKV_KV_FP8 or PKV_KV_BF16");
+    if (!known_kv(kv_dtype))
+        return fail(PKV_ERR_INVALID_ARG, "kv_dtype must be PKV_KV_FP8, PKV_KV_BF16 or PKV_KV_INT4");
     if (!cluster_size || !ctas || !launches)
         return fail(PKV_ERR_INVALID_ARG, "null output pointer");
     if (batch < 1) return fail(PKV_ERR_INVALID_ARG, "batch must be >= 1");
@@ -840,8 +1109,8 @@ pkv_status paged_decode_attn_plan(int32_t kv_dtype, int32_t batch, int32_t num_q
     if (num_ctas < -pkv::kMaxCluster)
         return fail(PKV_ERR_INVALID_ARG, "num_ctas must be >= %d", -pkv::kMaxCluster);
     AttnPlan plan;
-    st = plan_attention(kv_dtype == PKV_KV_FP8, batch, num_kv_heads, group, head_dim, max_pages,
-                        page_size, num_ctas, &plan);
+    st = plan_attention(kv_dtype, batch, num_kv_heads, group, head_dim, max_pages, page_size, 0, 0,
+                        num_ctas, &plan);
     if (st != PKV_OK) return st;
     *cluster_size = plan.cluster;
     *ctas = plan.cluster > 0 ? plan.cluster * plan.nclusters : plan.grid;
@@ -852,8 +1121,8 @@ pkv_status paged_decode_attn_plan(int32_t kv_dtype, int32_t batch, int32_t num_q
 size_t paged_decode_attn_workspace_size(int32_t kv_dtype, int32_t batch, int32_t num_q_heads,
                                         int32_t num_kv_heads, int32_t head_dim,
                                         int32_t num_ctas) {
-    if (kv_dtype != PKV_KV_FP8 && kv_dtype != PKV_KV_BF16) {
-        fail(PKV_ERR_INVALID_ARG, "kv_dtype must be PKV_KV_FP8 or PKV_KV_BF16");
+    if (!known_kv(kv_dtype)) {
+        fail(PKV_ERR_INVALID_ARG, "kv_dtype must be PKV_KV_FP8, PKV_KV_BF16 or PKV_KV_INT4");
         return 0;
     }
     if (batch < 0 || num_kv_heads < 1 || num_q_heads < 1 || num_q_heads % num_kv_heads != 0 ||
@@ -867,9 +1136,16 @@ size_t paged_decode_attn_workspace_size(int32_t kv_dtype, int32_t batch, int32_t
         return 0;
     }
     int grid = num_ctas > 0 ? num_ctas : 0;   // cluster mode (< 0) needs no more than the default
-    const bool fp8 = kv_dtype == PKV_KV_FP8;
-    const int kv_per_item = pkv::kv_heads_per_item(fp8, num_kv_heads, group);
-    if (grid == 0 && default_ctas(fp8, head_dim, group, kv_per_item, &grid) != PKV_OK) return 0;
+    const int kv_per_item = pkv::kv_heads_per_item(kv_dtype, num_kv_heads, group);
+    if (grid == 0) {
+        // the larger of the grids without and with a window: one workspace serves both calls
+        for (const bool window : {false, true}) {
+            int ctas = 0;
+            if (default_ctas(variant_of(kv_dtype, head_dim, group, kv_per_item, window), &ctas) != PKV_OK)
+                return 0;
+            grid = std::max(grid, ctas);
+        }
+    }
     return pkv::workspace_layout(batch, group, num_kv_heads, kv_per_item, head_dim, grid).total;
 }
 
@@ -881,9 +1157,10 @@ pkv_status paged_decode_attn_fp8(const uint16_t* q, const uint8_t* k_cache,
                                  int32_t num_pages, float sm_scale, const uint8_t* abort,
                                  uint16_t* out, float* lse, void* workspace,
                                  size_t workspace_bytes, int32_t num_ctas, void* stream) {
-    return attn_impl(true, q, k_cache, v_cache, k_scale, v_scale, page_table, max_pages, seq_lens,
-                     batch, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, sm_scale,
-                     abort, out, lse, workspace, workspace_bytes, num_ctas, stream);
+    return attn_impl({PKV_KV_FP8, k_cache, v_cache, k_scale, v_scale, nullptr, nullptr}, q,
+                     page_table, max_pages, seq_lens, batch, num_q_heads, num_kv_heads, head_dim,
+                     page_size, num_pages, sm_scale, 0, 0, abort, out, lse, workspace,
+                     workspace_bytes, num_ctas, stream);
 }
 
 size_t paged_decode_attn_fp8_prefix_workspace_size(int32_t batch, int32_t num_q_heads,
@@ -899,7 +1176,9 @@ size_t paged_decode_attn_fp8_prefix_workspace_size(int32_t batch, int32_t num_q_
         return paged_decode_attn_workspace_size(PKV_KV_FP8, batch, num_q_heads, num_kv_heads,
                                                 head_dim, num_ctas);
     int grid = num_ctas;
-    if (grid == 0 && default_ctas(true, head_dim, group, 2, &grid) != PKV_OK) return 0;
+    if (grid == 0 &&
+        default_ctas(variant_of(PKV_KV_FP8, head_dim, group, 2, false), &grid) != PKV_OK)
+        return 0;
     const size_t base = pkv::workspace_layout(batch, group, num_kv_heads, 2, head_dim, grid).total;
     return prefix_layout(base, batch, num_kv_heads, group).total;
 }
@@ -928,9 +1207,77 @@ pkv_status paged_decode_attn_bf16(const uint16_t* q, const uint16_t* k_cache,
                                   const uint8_t* abort, uint16_t* out, float* lse,
                                   void* workspace, size_t workspace_bytes, int32_t num_ctas,
                                   void* stream) {
-    return attn_impl(false, q, k_cache, v_cache, 1.f, 1.f, page_table, max_pages, seq_lens, batch,
-                     num_q_heads, num_kv_heads, head_dim, page_size, num_pages, sm_scale, abort,
-                     out, lse, workspace, workspace_bytes, num_ctas, stream);
+    return attn_impl({PKV_KV_BF16, k_cache, v_cache, 1.f, 1.f, nullptr, nullptr}, q, page_table,
+                     max_pages, seq_lens, batch, num_q_heads, num_kv_heads, head_dim, page_size,
+                     num_pages, sm_scale, 0, 0, abort, out, lse, workspace, workspace_bytes,
+                     num_ctas, stream);
+}
+
+pkv_status paged_decode_attn_int4(const uint16_t* q, const uint8_t* k_codes,
+                                  const uint16_t* k_params, const uint8_t* v_codes,
+                                  const uint16_t* v_params, const int32_t* page_table,
+                                  int32_t max_pages, const int32_t* seq_lens, int32_t batch,
+                                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                  int32_t page_size, int32_t num_pages, float sm_scale,
+                                  const uint8_t* abort, uint16_t* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, int32_t num_ctas, void* stream) {
+    return attn_impl({PKV_KV_INT4, k_codes, v_codes, 1.f, 1.f, k_params, v_params}, q, page_table,
+                     max_pages, seq_lens, batch, num_q_heads, num_kv_heads, head_dim, page_size,
+                     num_pages, sm_scale, 0, 0, abort, out, lse, workspace, workspace_bytes,
+                     num_ctas, stream);
+}
+
+pkv_status paged_decode_attn_fp8_window(const uint16_t* q, const uint8_t* k_cache,
+                                        const uint8_t* v_cache, float k_scale, float v_scale,
+                                        const int32_t* page_table, int32_t max_pages,
+                                        const int32_t* seq_lens, int32_t batch,
+                                        int32_t num_q_heads, int32_t num_kv_heads,
+                                        int32_t head_dim, int32_t page_size, int32_t num_pages,
+                                        float sm_scale, int32_t window, int32_t sinks,
+                                        const uint8_t* abort, uint16_t* out, float* lse,
+                                        void* workspace, size_t workspace_bytes, int32_t num_ctas,
+                                        void* stream) {
+    const pkv_status st = check_window(window, sinks);
+    if (st != PKV_OK) return st;
+    return attn_impl({PKV_KV_FP8, k_cache, v_cache, k_scale, v_scale, nullptr, nullptr}, q,
+                     page_table, max_pages, seq_lens, batch, num_q_heads, num_kv_heads, head_dim,
+                     page_size, num_pages, sm_scale, window, sinks, abort, out, lse, workspace,
+                     workspace_bytes, num_ctas, stream);
+}
+
+pkv_status paged_decode_attn_bf16_window(const uint16_t* q, const uint16_t* k_cache,
+                                         const uint16_t* v_cache, const int32_t* page_table,
+                                         int32_t max_pages, const int32_t* seq_lens, int32_t batch,
+                                         int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t page_size, int32_t num_pages,
+                                         float sm_scale, int32_t window, int32_t sinks,
+                                         const uint8_t* abort, uint16_t* out, float* lse,
+                                         void* workspace, size_t workspace_bytes, int32_t num_ctas,
+                                         void* stream) {
+    const pkv_status st = check_window(window, sinks);
+    if (st != PKV_OK) return st;
+    return attn_impl({PKV_KV_BF16, k_cache, v_cache, 1.f, 1.f, nullptr, nullptr}, q, page_table,
+                     max_pages, seq_lens, batch, num_q_heads, num_kv_heads, head_dim, page_size,
+                     num_pages, sm_scale, window, sinks, abort, out, lse, workspace,
+                     workspace_bytes, num_ctas, stream);
+}
+
+pkv_status paged_decode_attn_int4_window(const uint16_t* q, const uint8_t* k_codes,
+                                         const uint16_t* k_params, const uint8_t* v_codes,
+                                         const uint16_t* v_params, const int32_t* page_table,
+                                         int32_t max_pages, const int32_t* seq_lens, int32_t batch,
+                                         int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t page_size, int32_t num_pages,
+                                         float sm_scale, int32_t window, int32_t sinks,
+                                         const uint8_t* abort, uint16_t* out, float* lse,
+                                         void* workspace, size_t workspace_bytes, int32_t num_ctas,
+                                         void* stream) {
+    const pkv_status st = check_window(window, sinks);
+    if (st != PKV_OK) return st;
+    return attn_impl({PKV_KV_INT4, k_codes, v_codes, 1.f, 1.f, k_params, v_params}, q, page_table,
+                     max_pages, seq_lens, batch, num_q_heads, num_kv_heads, head_dim, page_size,
+                     num_pages, sm_scale, window, sinks, abort, out, lse, workspace,
+                     workspace_bytes, num_ctas, stream);
 }
 
 pkv_status int4_dequant_gemv(const uint16_t* x, const uint8_t* w_tiles, const uint16_t* scales,

@@ -51,23 +51,30 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
-template <bool kFp8, int kD, int kGP, int kH>
+template <int kKv, int kD, int kGP, int kH>
 struct AttnCfg {
-    static constexpr int kElem = kFp8 ? 1 : 2;
-    static constexpr int kRowBytes = kD * kElem;                 // 64, 128 or 256
-    static constexpr int kBoxBytes = kFp8 ? kRowBytes : 128;     // TMA box inner bytes
+    static constexpr bool kFp8 = kKv == kKvFp8;
+    static constexpr bool kInt4 = kKv == kKvInt4;
+    static constexpr int kRowBytes = kInt4 ? kD / 2 : (kFp8 ? kD : 2 * kD);  // 32 to 256
+    static constexpr int kBoxBytes = kKv == kKvBf16 ? 128 : kRowBytes;       // TMA box inner bytes
     static constexpr int kSubTiles = kRowBytes / kBoxBytes;      // 2 for BF16 D=128
-    static constexpr int kSwizzle = kBoxBytes;                   // 128 or 64
+    static constexpr int kSwizzle = kBoxBytes;                   // 128, 64 or 32 (none)
     static constexpr int kSubTileBytes = kChunkTokens * kBoxBytes;
     static constexpr int kHeadTileBytes = kChunkTokens * kRowBytes;  // one KV head of a chunk
     static constexpr int kTileBytes = kH * kHeadTileBytes;           // K (or V) of a stage
-    static constexpr int kStageBytes = 2 * kTileBytes;
+    // INT4: the (scale, minimum) pairs of a token's groups follow the codes of
+    // a stage, K's rows first, then V's.
+    static constexpr int kGroups = kInt4 ? kD / kInt4Group : 1;
+    static constexpr int kParRowBytes = kInt4 ? 4 * kGroups : 0;
+    static constexpr int kParTileBytes = kH * kChunkTokens * kParRowBytes;
+    static constexpr int kStageBytes = (2 * (kTileBytes + kParTileBytes) + 1023) / 1024 * 1024;
     // Pipeline depth and resident CTAs per SM, chosen by measurement on B200:
     // resident warps matter more than depth (each CTA keeps up to kStages
     // chunks in flight), so the depth is the largest that still lets
     // kMinBlocks CTAs share an SM's 228 KB of shared memory.
-    static constexpr int kStages = kFp8 ? (kD == 128 ? (kH == 2 ? 3 : 4) : (kH == 2 ? 3 : 6))
-                                        : (kD == 128 ? 2 : 4);
+    static constexpr int kStages = kInt4 ? (kD == 128 ? (kH == 2 ? 5 : 6) : 8)
+                                   : kFp8 ? (kD == 128 ? (kH == 2 ? 3 : 4) : (kH == 2 ? 3 : 6))
+                                          : (kD == 128 ? 2 : 4);
     static constexpr int kMinBlocks = (kFp8 && kGP == 8 && kH == 1) ? 3 : 2;
     // The epilogue's cross-warp reduction of O (4 warps x kGP heads x kD fp32)
     // reuses the stage of the segment's last chunk when it fits there (a
@@ -96,7 +103,8 @@ struct AttnCfg {
     // 16 live registers to a variant with the 2-CTA register budget (168);
     // otherwise (more words, or the tighter 3-CTA budget) at the segment's
     // start.
-    static constexpr int kQWords = kFp8 ? (kGP / 8) * (kD / 64) * 8 : (kGP / 8) * (kD / 16) * 2;
+    static constexpr int kQWords = kKv != kKvBf16 ? (kGP / 8) * (kD / 64) * 8
+                                                  : (kGP / 8) * (kD / 16) * 2;
     static constexpr bool kEarlyQ = kQWords <= 16 && kMinBlocks == 2;
     static_assert(kD == 64 || kD == 128, "head_dim");
     static_assert(kGP == 8 || kGP == 16, "group pad");
@@ -108,37 +116,71 @@ struct AttnCfg {
 // per accumulator layout so that one store instruction's lanes (and each
 // 8-lane phase of a 16-byte store) reach distinct banks: FP8 D=128 stores
 // units 4g+k, FP8 D=64 units 2g+k, BF16 single words of units 4mb+g/4 (+2).
-template <bool kFp8, int kD>
+// INT4 stores units 16 group + 2g+k: the pattern of FP8 D=64 at both sizes.
+template <int kKv, int kD>
 __device__ __forceinline__ uint32_t red_swizzle(int c) {
-    if constexpr (!kFp8) return 2u * c;
-    else if constexpr (kD == 128) return static_cast<uint32_t>(c);
+    if constexpr (kKv == kKvBf16) return 2u * c;
+    else if constexpr (kKv == kKvFp8 && kD == 128) return static_cast<uint32_t>(c);
     else return static_cast<uint32_t>((c & 1) | ((c & 2) << 1));
 }
 
 // Token permutation inside an 8-row group: row tau(n) feeds MMA column n.
-__device__ __forceinline__ int tau(int n) { return n ^ ((n & 1) << 2); }
+// INT4 rows are 64 (D = 128, 64-byte swizzle) or 32 bytes: K is read 8 bytes a
+// lane, half a warp (4 rows) at a time, V 4 bytes a lane from the 4 rows of the
+// even (then the odd) columns, and either 4 rows must fall on 4 different
+// 32-byte quarters of the 128 banks: rows r with r % 2 and r / 4 different
+// (D = 128: 0 1 4 5 3 2 7 6), or with r % 4 different (D = 64: 0 1 2 3 5 4 7 6).
+template <int kKv, int kD>
+__device__ __forceinline__ int tau(int n) {
+    if constexpr (kKv == kKvInt4 && kD == 128)
+        return ((n & 2) << 1) | ((n & 4) >> 1) | ((n ^ (n >> 2)) & 1);
+    else if constexpr (kKv == kKvInt4)
+        return n ^ (n >> 2);
+    else
+        return n ^ ((n & 1) << 2);
+}
+
+// Units are counted over the chunks that hold a visible token.  With a window,
+// those are the first `a` chunks (sinks) and the ones from a + gap on; unit ch
+// of a request is chunk real(ch).
+struct WindowGap {
+    int a, gap;
+};
+// Visible tokens of a request of `len` tokens: the last `window` ones and the
+// first `sinks`.  Chunks [a, a + gap) hold none of them.
+__device__ __forceinline__ WindowGap window_gap(int len, int window, int sinks) {
+    const int lo = max(len - window, 0);                  // first token of the window
+    const int w = lo / kChunkTokens;
+    const int s = (min(sinks, lo) + kChunkTokens - 1) / kChunkTokens;
+    return {s, max(w - s, 0)};
+}
 
 struct Segment {
     int b, h, c0, c1, n, L;
+    int a, gap;
+    __device__ __forceinline__ int real(int ch) const { return ch < a ? ch : ch + gap; }
 };
 
 // Walks a CTA's unit range [u, u_hi) segment by segment.  Every warp runs an
 // identical copy, so producer and consumers agree without communicating.
 // Units of an item are its chunks from the request's first chunk (0, or
 // chunk_begin[b] in shared-prefix mode) to its last.
+template <bool kWin>
 struct Walker {
     const int32_t* seq_lens;
     const int32_t* chunk_begin;   // null: every request from chunk 0
     int64_t max_tokens;
     int num_kv_heads;
     int batch;
+    int window, sinks;            // kWin only
     int b, h, ch, n, L, cb;
     int64_t u, u_hi;
 
     __device__ __forceinline__ int chunks_of(int32_t len) const {
-        return (len >= 1 && static_cast<int64_t>(len) <= max_tokens)
-                   ? (len + kChunkTokens - 1) / kChunkTokens
-                   : 0;
+        if (!(len >= 1 && static_cast<int64_t>(len) <= max_tokens)) return 0;
+        const int all = (len + kChunkTokens - 1) / kChunkTokens;
+        if constexpr (kWin) return all - window_gap(len, window, sinks).gap;
+        return all;
     }
     __device__ __forceinline__ int begin_of(int bb) const {
         return chunk_begin != nullptr ? chunk_begin[bb] : 0;
@@ -175,6 +217,13 @@ struct Walker {
         s.c1 = ch + take;
         s.n = n;
         s.L = L;
+        if constexpr (kWin) {
+            const WindowGap g = window_gap(L, window, sinks);
+            s.a = g.a;
+            s.gap = g.gap;
+        } else {
+            s.a = s.gap = 0;
+        }
         u += take;
         ch += take;
         if (u < u_hi && ch == n) {
@@ -240,9 +289,9 @@ struct PageWindow {
 // in (rank, record) order each split item's records form one run; the runs'
 // outputs are spread over all threads of the cluster.  Kept out of line so
 // that nothing it needs stays live through the partial kernel's main loop.
-template <bool kFp8, int kD, int kGP, int kH>
+template <int kKv, int kD, int kGP, int kH>
 __device__ __noinline__ void attn_cluster_reduce(const AttnArgs& a, uint8_t* smem) {
-    using C = AttnCfg<kFp8, kD, kGP, kH>;
+    using C = AttnCfg<kKv, kD, kGP, kH>;
     constexpr int K = kMaxCluster;
     constexpr int kWarps = kAttnThreads / 32;
     const int tid = threadIdx.x;
@@ -383,11 +432,13 @@ __device__ __noinline__ void attn_cluster_reduce(const AttnArgs& a, uint8_t* sme
 // ---------------------------------------------------------------------------
 // the split-K partial kernel
 // ---------------------------------------------------------------------------
-template <bool kFp8, int kD, int kGP, int kH>
-__global__ void __launch_bounds__(kAttnThreads, (AttnCfg<kFp8, kD, kGP, kH>::kMinBlocks))
+template <int kKv, int kD, int kGP, int kH, bool kWin>
+__global__ void __launch_bounds__(kAttnThreads, (AttnCfg<kKv, kD, kGP, kH>::kMinBlocks))
 attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ AttnArgs a) {
-    using C = AttnCfg<kFp8, kD, kGP, kH>;
+    using C = AttnCfg<kKv, kD, kGP, kH>;
+    constexpr bool kFp8 = C::kFp8, kInt4 = C::kInt4;
+    constexpr int kPR = C::kParRowBytes;   // INT4: bytes of a token's parameters
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -439,7 +490,9 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
 
     // ---- partition: exclusive scan of chunk counts over the batch --------
-    Walker walk;
+    Walker<kWin> walk;
+    walk.window = a.window;
+    walk.sinks = a.sinks;
     walk.seq_lens = a.seq_lens;
     walk.chunk_begin = a.chunk_begin;
     walk.max_tokens = max_tokens;
@@ -529,6 +582,17 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const bool joint = (kH == 2) && (box_rows == 2 * kChunkTokens);
     const int boxes = joint ? 1 : kChunkTokens / box_rows;
 
+    // With a window: whether the box_rows tokens from tok0 on are all hidden
+    // (their page-table entry is then not used).
+    auto hidden_box = [&](int len, int tok0) {
+        if constexpr (kWin) {
+            const int lo = len - a.window;
+            return tok0 >= a.sinks && tok0 + (joint ? kChunkTokens : box_rows) <= lo;
+        } else {
+            return false;
+        }
+    };
+
     if (warp == kConsumerWarps) {
         // ================= producer warp =================
         prefetch_tensormap(&tmap_k);
@@ -537,17 +601,19 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         win.reset(nullptr);
         // L2 prefetch of the first S chunks, before the dependency wait.
         {
-            Walker w2 = walk;
+            Walker<kWin> w2 = walk;
             Segment s;
             int count = 0;
             while (count < S && w2.next(s)) {
                 win.reset(a.page_table + static_cast<int64_t>(s.b) * a.max_pages);
                 const int npages = (s.L + P - 1) / P;
                 for (int ch = s.c0; ch < s.c1 && count < S; ++ch, ++count) {
+                    const int rc = s.real(ch);
                     for (int i = 0; i < boxes; ++i) {
-                        const int tok0 = ch * kChunkTokens + i * box_rows;
+                        const int tok0 = rc * kChunkTokens + i * box_rows;
                         const int j = tok0 / P;
                         if (j >= npages) break;
+                        if (hidden_box(s.L, tok0)) continue;
                         const int32_t pid = win.get(j, npages, lane);
                         if (lane == 0 && pid >= 0 && pid < a.num_pages) {
                             for (int kv = 0; kv < (joint ? 1 : kH); ++kv) {
@@ -555,6 +621,11 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                 for (int st = 0; st < C::kSubTiles; ++st) {
                                     tma_prefetch_l2_2d(&tmap_k, st * 64, y);
                                     tma_prefetch_l2_2d(&tmap_v, st * 64, y);
+                                }
+                                if constexpr (kInt4) {
+                                    const int64_t off = static_cast<int64_t>(y) * kPR;
+                                    bulk_prefetch_l2(a.k_params + off, box_rows * kPR);
+                                    bulk_prefetch_l2(a.v_params + off, box_rows * kPR);
                                 }
                             }
                         }
@@ -569,7 +640,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // the L2 prefetch above already loaded for this row is kept)
         auto load_meta = [&](const Segment& sg, PageWindow& w) {
             const int32_t* row = a.page_table + static_cast<int64_t>(sg.b) * a.max_pages;
-            const int j0 = sg.c0 * kChunkTokens / P;
+            const int j0 = sg.real(sg.c0) * kChunkTokens / P;
             if (w.row != row || w.base != j0) {
                 w.reset(row);
                 w.preload(j0, (sg.L + P - 1) / P, lane);
@@ -609,6 +680,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 const uint32_t kdst = smem_addr(smem + stage * C::kStageBytes);
                 const uint32_t vdst = kdst + C::kTileBytes;
+                const int rc = s.real(ch);
                 uint32_t bytes = 0;
                 int bad = 0;
                 int32_t pids[4];
@@ -616,15 +688,16 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 for (int i = 0; i < 4; ++i) {
                     pids[i] = -1;
                     if (i < boxes) {
-                        const int tok0 = ch * kChunkTokens + i * box_rows;
+                        const int tok0 = rc * kChunkTokens + i * box_rows;
                         const int j = tok0 / P;
-                        if (j < npages) {
+                        if (j < npages && !hidden_box(s.L, tok0)) {
                             pids[i] = win.get(j, npages, lane);
                             if (pids[i] < 0 || pids[i] >= a.num_pages) {
                                 bad = 1;
                                 pids[i] = -1;
                             } else {
-                                bytes += 2u * C::kSubTiles * box_rows * C::kBoxBytes * (joint ? 1 : kH);
+                                bytes += 2u * (C::kSubTiles * C::kBoxBytes + kPR) * box_rows *
+                                         (joint ? 1 : kH);
                             }
                         }
                     }
@@ -635,7 +708,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (pids[i] < 0) continue;
-                        const int tok0 = ch * kChunkTokens + i * box_rows;
+                        const int tok0 = rc * kChunkTokens + i * box_rows;
                         for (int kv = 0; kv < (joint ? 1 : kH); ++kv) {
                             const int32_t y = (pids[i] * Hkv + s.h * kH + kv) * P + (tok0 % P);
                             for (int st = 0; st < C::kSubTiles; ++st) {
@@ -643,6 +716,14 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                                      i * box_rows * C::kBoxBytes;
                                 tma_load_2d(kdst + off, &tmap_k, st * 64, y, &full_bar[stage]);
                                 tma_load_2d(vdst + off, &tmap_v, st * 64, y, &full_bar[stage]);
+                            }
+                            if constexpr (kInt4) {
+                                const uint32_t pdst = vdst + C::kTileBytes +
+                                                      (kv * kChunkTokens + i * box_rows) * kPR;
+                                const int64_t src = static_cast<int64_t>(y) * kPR;
+                                bulk_load(pdst, a.k_params + src, box_rows * kPR, &full_bar[stage]);
+                                bulk_load(pdst + C::kParTileBytes, a.v_params + src, box_rows * kPR,
+                                          &full_bar[stage]);
                             }
                         }
                     }
@@ -654,7 +735,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             s = sn;
             have = have_next;
         }
-        if (a.cluster_size > 0) attn_cluster_reduce<kFp8, kD, kGP, kH>(a, smem);
+        if (a.cluster_size > 0) attn_cluster_reduce<kKv, kD, kGP, kH>(a, smem);
         return;
     }
 
@@ -682,21 +763,37 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // Fixed shared-memory offsets of this thread's K and V reads.
     uint32_t k_off[2][kD / 64];       // FP8: rows tau(g), 8+tau(g); chunks c, 4+c
     uint32_t v_off[4];                // FP8: rows tau(2c), tau(2c+1), 8+.., 8+..; chunk g
+    auto tok = [](int n) { return tau<kKv, kD>(n); };
     if constexpr (kFp8) {
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int part = 0; part < kD / 64; ++part)
-                k_off[half][part] = swz<C::kRowBytes, C::kSwizzle>(row0 + 8 * half + tau(g),
+                k_off[half][part] = swz<C::kRowBytes, C::kSwizzle>(row0 + 8 * half + tok(g),
                                                                    16 * (4 * part + c));
-        const int vr[4] = {row0 + tau(2 * c), row0 + tau(2 * c + 1), row0 + 8 + tau(2 * c),
-                           row0 + 8 + tau(2 * c + 1)};
+        const int vr[4] = {row0 + tok(2 * c), row0 + tok(2 * c + 1), row0 + 8 + tok(2 * c),
+                           row0 + 8 + tok(2 * c + 1)};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             v_off[i] = swz<C::kRowBytes, C::kSwizzle>(vr[i], (kD == 128 ? 16 : 8) * g);
     }
+    // INT4: per group, K bytes [8c, 8c+8) of rows tau(g), 8+tau(g); V bytes
+    // [4g, 4g+4) of rows tau(2c), tau(2c+1), 8+.., 8+..
+    uint32_t k4_off[2][C::kGroups], v4_off[4][C::kGroups];
+    if constexpr (kInt4) {
+#pragma unroll
+        for (int gr = 0; gr < C::kGroups; ++gr) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                k4_off[i][gr] = swz<C::kRowBytes, C::kSwizzle>(row0 + 8 * i + tok(g), 32 * gr + 8 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v4_off[i][gr] = swz<C::kRowBytes, C::kSwizzle>(
+                    row0 + 8 * (i >> 1) + tok(2 * c + (i & 1)), 32 * gr + 4 * g);
+        }
+    }
 
-    // This warp's query rows of a segment as raw words: FP8, per n-block and
+    // This warp's query rows of a segment as raw words: FP8 and INT4, per n-block and
     // 64-dim part the 16 bf16 dims [16c, 16c+16) (8 words); BF16, the two
     // B-operand words of each k-step.  Heads past the group read as zero.
     constexpr int kQWords = C::kQWords;
@@ -707,7 +804,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const int hh = g + 8 * nb;
             const bool valid = hh < G;
             const uint16_t* qrow = a.q + (hw0 + (valid ? hh : 0)) * kD;
-            if constexpr (kFp8) {
+            if constexpr (kKv != kKvBf16) {
 #pragma unroll
                 for (int part = 0; part < kD / 64; ++part) {
                     const uint4* src = reinterpret_cast<const uint4*>(qrow + part * 64 + 16 * c);
@@ -802,12 +899,13 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // ---- Q^T as the B operand: column n = head g (+8 per n-block) -----
         uint32_t qb[kNB][kKS][2];
         float qs[kNB][2];   // score scale of S columns 2c and 2c+1
+        float qm[kNB][C::kGroups][2];   // INT4: scaled sum of the group's query dims, same columns
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb) {
             float my_scale;
-            if constexpr (kFp8) {
+            if constexpr (kKv != kKvBf16) {
                 // word j of the B operand holds dims D_c[4j..4j+3] of the
-                // permuted contraction: this thread's dims in order
+                // permuted contraction (FP8): this thread's dims in order
                 float v[kD / 4];
 #pragma unroll
                 for (int k = 0; k < kD / 8; ++k) {
@@ -823,20 +921,50 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 // 2^shift brings amax into [128, 256): with amax = f 2^e,
                 // f in [0.5, 1), shift = 8 - e, where e comes from the
                 // exponent field (a subnormal amax reads as e = -126, which
-                // the clamp maps to the same shift as its true exponent)
+                // the clamp maps to the same shift as its true exponent).
+                // INT4 brings it into [4096, 8192): half its dims are then
+                // divided by 16, which the wider range absorbs.
+                constexpr int kTop = kInt4 ? 13 : 8;
                 int shift = 0;
                 if (amax > 0.f && isfinite(amax)) {
                     const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu) - 126;
-                    shift = min(60, max(-126, 8 - e));
+                    shift = min(60, max(-126, kTop - e));
                 }
                 // scaling by an exact power of two rounds like ldexp
                 const float up = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
+                if constexpr (kInt4) {
+                    // k-step 4 part + i takes nibble i of the low and of the high
+                    // half of K words 0 and 1: dims i, i + 4 and 8 + i, 12 + i of
+                    // the thread's 16.  Odd i reads 16 times the code (see below).
 #pragma unroll
-                for (int j = 0; j < kKS; ++j) {
-                    qb[nb][j][0] = pack_f16x2(v[4 * j] * up, v[4 * j + 1] * up);
-                    qb[nb][j][1] = pack_f16x2(v[4 * j + 2] * up, v[4 * j + 3] * up);
+                    for (int part = 0; part < C::kGroups; ++part) {
+                        const float* w = v + 16 * part;
+                        float sum = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) sum += w[k];
+                        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                        sum *= a.qk_scale;
+                        qm[nb][part][0] = __shfl_sync(0xffffffffu, sum, 4 * (2 * c));
+                        qm[nb][part][1] = __shfl_sync(0xffffffffu, sum, 4 * (2 * c + 1));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float u = (i & 1) ? up * 0.0625f : up;
+                            qb[nb][4 * part + i][0] = pack_f16x2(w[i] * u, w[i + 4] * u);
+                            qb[nb][4 * part + i][1] = pack_f16x2(w[8 + i] * u, w[12 + i] * u);
+                        }
+                    }
+                    // (the codes read as code * 2^-24)
+                    my_scale = a.qk_scale * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23) *
+                               0x1p24f;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kKS; ++j) {
+                        qb[nb][j][0] = pack_f16x2(v[4 * j] * up, v[4 * j + 1] * up);
+                        qb[nb][j][1] = pack_f16x2(v[4 * j + 2] * up, v[4 * j + 3] * up);
+                    }
+                    my_scale = a.qk_scale * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
                 }
-                my_scale = a.qk_scale * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
             } else {
 #pragma unroll
                 for (int j = 0; j < kKS; ++j) {
@@ -865,14 +993,33 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             l[nb][0] = l[nb][1] = 0.f;
             lr[nb][0] = lr[nb][1] = 0.f;
         }
+        // INT4: O holds sum_t w_t s_t code_t / vref, with vref (a power of two,
+        // common to the warp) keeping the f16 weights w_t s_t / vref in range, and
+        // vb the part of the groups' minima, sum_t w_t m_t, in binary32.
+        float vref = 0.f, vinv = 0.f, vbias[kNB][C::kGroups][2];
+        if constexpr (kInt4) {
+#pragma unroll
+            for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+                for (int gr = 0; gr < C::kGroups; ++gr) vbias[nb][gr][0] = vbias[nb][gr][1] = 0.f;
+        }
         int poisoned = 0;
 
         for (int ch = s.c0; ch < s.c1; ++ch, ++it) {
             const int stage = it % S;
             wait_or_give_up(&full_bar[stage], (it / S) & 1, cta_failed, a.ws_status);
             poisoned |= stage_bad_rd[stage];
-            const int n_valid = min(kChunkTokens, s.L - ch * kChunkTokens);
-            const bool tail = n_valid < kChunkTokens;
+            const int n_valid = min(kChunkTokens, s.L - s.real(ch) * kChunkTokens);
+            // with a window, tokens [hid0, hid1) of the chunk are hidden
+            int hid0 = 0, hid1 = 0;
+            if constexpr (kWin) {
+                hid0 = max(a.sinks - s.real(ch) * kChunkTokens, 0);
+                hid1 = s.L - a.window - s.real(ch) * kChunkTokens;
+            }
+            const bool tail = n_valid < kChunkTokens || (kWin && hid0 < min(hid1, kChunkTokens));
+            auto masked = [&](int t) {
+                return t >= n_valid || (kWin && t >= hid0 && t < hid1);
+            };
             const uint32_t kb_head = smem_addr(smem + stage * C::kStageBytes) + kvh_w * C::kHeadTileBytes;
             const uint32_t vb_head = kb_head + C::kTileBytes;
 #pragma unroll
@@ -880,8 +1027,8 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const int rb = row0 + 16 * t;
             // FP8 offsets are relative to the warp's first tile; 16 rows on, the
             // swizzle pattern repeats, so the next tile is a plain offset
-            const uint32_t kb = kb_head + (kFp8 ? t * 16 * C::kRowBytes : 0);
-            const uint32_t vb = vb_head + (kFp8 ? t * 16 * C::kRowBytes : 0);
+            const uint32_t kb = kb_head + (kKv != kKvBf16 ? t * 16 * C::kRowBytes : 0);
+            const uint32_t vb = vb_head + (kKv != kKvBf16 ? t * 16 * C::kRowBytes : 0);
 
             // ---- S[16 tokens][8 heads] = K Q^T, two accumulator chains ------
             float acc[kNB][2][4];
@@ -907,6 +1054,26 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     for (int nb = 0; nb < kNB; ++nb)
                         mma_f16(acc[nb][j & 1], a0, a1, a2, a3, qb[nb][j][0], qb[nb][j][1]);
                 }
+            } else if constexpr (kInt4) {
+                // A 4-bit code in bits 0-3 (4-7) of an f16 whose other bits are
+                // zero reads as the subnormal code * 2^-24 (* 2^-20), exactly: one
+                // AND turns two codes of a word into an operand pair.
+#pragma unroll
+                for (int gr = 0; gr < C::kGroups; ++gr) {
+                    uint2 x = lds64(kb + k4_off[0][gr]);
+                    uint2 y = lds64(kb + k4_off[1][gr]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t msk = (i & 1) ? 0x00F000F0u : 0x000F000Fu;
+                        if (i == 2) {
+                            x.x >>= 8; x.y >>= 8; y.x >>= 8; y.y >>= 8;
+                        }
+#pragma unroll
+                        for (int nb = 0; nb < kNB; ++nb)
+                            mma_f16(acc[nb][C::kGroups == 2 ? gr : (i & 1)], x.x & msk, y.x & msk,
+                                    x.y & msk, y.y & msk, qb[nb][4 * gr + i][0], qb[nb][4 * gr + i][1]);
+                    }
+                }
             } else {
                 const int q8 = lane >> 3;
                 const int row = rb + 8 * (q8 & 1) + (lane & 7);
@@ -926,18 +1093,68 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // ---- online softmax over the 16 tokens, per head (log2 units) ----
             // p[nb][0..1]: token row g, heads 2c, 2c+1; p[nb][2..3]: row g + 8
             float p[kNB][4];
+            // INT4: V's (scale, minimum) of this thread's two tokens, per group
+            float vs[2][C::kGroups], vm[2][C::kGroups];
+            float vtop = 0.f;
+            if constexpr (kInt4) {
+                // s_t = qk_scale (sum_gr scale_t,gr (q . code)_gr + minimum_t,gr sum(q)_gr)
+                const uint32_t kp = kb_head + 2 * C::kTileBytes - kvh_w * C::kHeadTileBytes +
+                                    (kvh_w * kChunkTokens + rb + tok(g)) * kPR;
+                const uint32_t vp = kp + C::kParTileBytes;
+                uint32_t kw[2][2], vw[2][2];
 #pragma unroll
-            for (int nb = 0; nb < kNB; ++nb)
+                for (int i = 0; i < 2; ++i) {
+                    if constexpr (C::kGroups == 2) {
+                        const uint2 x = lds64(kp + 8 * i * kPR), y = lds64(vp + 8 * i * kPR);
+                        kw[i][0] = x.x; kw[i][1] = x.y; vw[i][0] = y.x; vw[i][1] = y.y;
+                    } else {
+                        kw[i][0] = lds32(kp + 8 * i * kPR); vw[i][0] = lds32(vp + 8 * i * kPR);
+                    }
+                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    p[nb][i] = (acc[nb][0][i] + acc[nb][1][i]) * qs[nb][i & 1];
+                for (int i = 0; i < 2; ++i) {
+                    float ks[C::kGroups], km[C::kGroups];
+#pragma unroll
+                    for (int gr = 0; gr < C::kGroups; ++gr) {
+                        bf16x2_to_f32x2(kw[i][gr], ks[gr], km[gr]);
+                        bf16x2_to_f32x2(vw[i][gr], vs[i][gr], vm[i][gr]);
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+                        for (int col = 0; col < 2; ++col) {
+                            float x = 0.f, y = 0.f;
+                            if constexpr (C::kGroups == 2) {
+                                x = ks[0] * acc[nb][0][2 * i + col] + ks[1] * acc[nb][1][2 * i + col];
+                                y = km[0] * qm[nb][0][col] + km[1] * qm[nb][1][col];
+                            } else {
+                                x = ks[0] * (acc[nb][0][2 * i + col] + acc[nb][1][2 * i + col]);
+                                y = km[0] * qm[nb][0][col];
+                            }
+                            p[nb][2 * i + col] = fmaf(x, qs[nb][col], y);
+                        }
+                }
+            } else {
+#pragma unroll
+                for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        p[nb][i] = (acc[nb][0][i] + acc[nb][1][i]) * qs[nb][i & 1];
+            }
             if (tail) {
-                const int t_lo = kFp8 ? rb + tau(g) : rb + g;
+                const int t_lo = kKv != kKvBf16 ? rb + tok(g) : rb + g;
                 const int t_hi = t_lo + 8;
 #pragma unroll
                 for (int nb = 0; nb < kNB; ++nb) {
-                    if (t_lo >= n_valid) p[nb][0] = p[nb][1] = kNegInf;
-                    if (t_hi >= n_valid) p[nb][2] = p[nb][3] = kNegInf;
+                    if (masked(t_lo)) p[nb][0] = p[nb][1] = kNegInf;
+                    if (masked(t_hi)) p[nb][2] = p[nb][3] = kNegInf;
+                }
+                if constexpr (kInt4) {
+#pragma unroll
+                    for (int gr = 0; gr < C::kGroups; ++gr) {
+                        if (masked(t_lo)) vs[0][gr] = vm[0][gr] = 0.f;
+                        if (masked(t_hi)) vs[1][gr] = vm[1][gr] = 0.f;
+                    }
                 }
             }
             // Lazy rescaling: the running max m (uniform over the warp, per head)
@@ -949,7 +1166,25 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
                 for (int col = 0; col < 2; ++col)
                     need |= fmaxf(p[nb][col], p[nb][col + 2]) > m[nb][col] + kRescaleThreshold;
+            if constexpr (kInt4) {
+#pragma unroll
+                for (int gr = 0; gr < C::kGroups; ++gr)
+                    vtop = fmaxf(vtop, fmaxf(fabsf(vs[0][gr]), fabsf(vs[1][gr])));
+                need |= vtop > 64.f * vref;
+            }
             if (__any_sync(0xffffffffu, need)) {
+                float vfix = 1.f;
+                if constexpr (kInt4) {
+                    // the largest scale so far as a power of two, within [2^-100, 2^126]
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1)
+                        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
+                    const uint32_t e = min(max(__float_as_uint(vtop) >> 23, 27u), 253u);
+                    const float now = fmaxf(vref, __uint_as_float(e << 23));
+                    vinv = __uint_as_float((254u - (__float_as_uint(now) >> 23)) << 23);
+                    vfix = vref * vinv;
+                    vref = now;
+                }
 #pragma unroll
                 for (int nb = 0; nb < kNB; ++nb) {
                     float alpha[2];
@@ -965,6 +1200,15 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         l[nb][col] *= alpha[col];
                         lr[nb][col] *= alpha[col];
                     }
+                    if constexpr (kInt4) {
+#pragma unroll
+                        for (int gr = 0; gr < C::kGroups; ++gr) {
+                            vbias[nb][gr][0] *= alpha[0];
+                            vbias[nb][gr][1] *= alpha[1];
+                        }
+                        alpha[0] *= vfix;
+                        alpha[1] *= vfix;
+                    }
 #pragma unroll
                     for (int mb = 0; mb < kMB; ++mb) {
                         o[nb][mb][0] *= alpha[0];
@@ -976,6 +1220,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
             // P^T as the PV B operand: k = token row, n = head g
             uint32_t pb[kNB][2];
+            uint32_t pb4[kNB][C::kGroups][2];   // INT4: weights times each group's scale
 #pragma unroll
             for (int nb = 0; nb < kNB; ++nb) {
 #pragma unroll
@@ -985,6 +1230,24 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 l[nb][0] += p[nb][0] + p[nb][2];
                 l[nb][1] += p[nb][1] + p[nb][3];
+                if constexpr (kInt4) {
+                    // f16 weights (2^-11 of each at most): a weight is at most 2^8 and
+                    // scale / vref below 64, so the product stays below 2^14
+#pragma unroll
+                    for (int gr = 0; gr < C::kGroups; ++gr) {
+                        const float w0 = vs[0][gr] * vinv, w1 = vs[1][gr] * vinv;
+                        pb4[nb][gr][0] =
+                            movmatrix_trans(pack_f16x2(p[nb][0] * w0, p[nb][1] * w0));
+                        pb4[nb][gr][1] =
+                            movmatrix_trans(pack_f16x2(p[nb][2] * w1, p[nb][3] * w1));
+#pragma unroll
+                        for (int col = 0; col < 2; ++col)
+                            vbias[nb][gr][col] = fmaf(p[nb][col], vm[0][gr],
+                                                      fmaf(p[nb][col + 2], vm[1][gr],
+                                                           vbias[nb][gr][col]));
+                    }
+                    continue;
+                }
                 uint32_t h01, h23;
                 float r0, r1, r2, r3;
                 if constexpr (kFp8) {
@@ -1021,11 +1284,11 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     }
                 }
                 if (tail) {
-                    const int vr[4] = {rb + tau(2 * c), rb + tau(2 * c + 1), rb + 8 + tau(2 * c),
-                                       rb + 8 + tau(2 * c + 1)};
+                    const int vr[4] = {rb + tok(2 * c), rb + tok(2 * c + 1), rb + 8 + tok(2 * c),
+                                       rb + 8 + tok(2 * c + 1)};
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        if (vr[r] >= n_valid)
+                        if (masked(vr[r]))
 #pragma unroll
                             for (int q = 0; q < kW; ++q) x[r][q] = 0u;
                 }
@@ -1044,14 +1307,40 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     for (int nb = 0; nb < kNB; ++nb)
                         mma_f16(o[nb][2 * q + 1], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
                 }
+            } else if constexpr (kInt4) {
+                // word [4g, 4g+4) of a group holds its dims 8g..8g+7: m-block
+                // 4 gr + i takes dims 2i (accumulator rows g, code * 2^-24) and
+                // 2i + 1 (rows g + 8, code * 2^-20).  Masked tokens have zero
+                // weights, and every code is a finite number.
+#pragma unroll
+                for (int gr = 0; gr < C::kGroups; ++gr) {
+                    uint32_t x[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) x[r] = lds32(vb + v4_off[r][gr]);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t sel = half ? 0x7632u : 0x5410u;
+                        uint32_t t01 = prmt(x[0], x[1], sel), t23 = prmt(x[2], x[3], sel);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                            for (int nb = 0; nb < kNB; ++nb)
+                                mma_f16(o[nb][4 * gr + 2 * half + k], t01 & 0x000F000Fu,
+                                        t01 & 0x00F000F0u, t23 & 0x000F000Fu, t23 & 0x00F000F0u,
+                                        pb4[nb][gr][0], pb4[nb][gr][1]);
+                            t01 >>= 8;
+                            t23 >>= 8;
+                        }
+                    }
+                }
             } else {
                 const int q8 = lane >> 3;
                 const int row = rb + 8 * (q8 >> 1) + (lane & 7);
                 const int t0 = rb + 2 * c;    // tokens of a0/a1: t0, t0+1; of a2/a3: t0+8, t0+9
                 uint32_t keep01 = 0xFFFFFFFFu, keep23 = 0xFFFFFFFFu;
                 if (tail) {
-                    keep01 = (t0 < n_valid ? 0x0000FFFFu : 0u) | (t0 + 1 < n_valid ? 0xFFFF0000u : 0u);
-                    keep23 = (t0 + 8 < n_valid ? 0x0000FFFFu : 0u) | (t0 + 9 < n_valid ? 0xFFFF0000u : 0u);
+                    keep01 = (masked(t0) ? 0u : 0x0000FFFFu) | (masked(t0 + 1) ? 0u : 0xFFFF0000u);
+                    keep23 = (masked(t0 + 8) ? 0u : 0x0000FFFFu) | (masked(t0 + 9) ? 0u : 0xFFFF0000u);
                 }
 #pragma unroll
                 for (int mb = 0; mb < kMB; ++mb) {
@@ -1100,7 +1389,17 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
                 vr += __shfl_xor_sync(0xffffffffu, vr, 16);
                 l[nb][col] = v;
-                lr[nb][col] = vr;
+                lr[nb][col] = kInt4 ? v : vr;   // (INT4 divides by the fp32 weights' sum)
+                if constexpr (kInt4) {
+#pragma unroll
+                    for (int gr = 0; gr < C::kGroups; ++gr) {
+                        float x = vbias[nb][gr][col];
+                        x += __shfl_xor_sync(0xffffffffu, x, 4);
+                        x += __shfl_xor_sync(0xffffffffu, x, 8);
+                        x += __shfl_xor_sync(0xffffffffu, x, 16);
+                        vbias[nb][gr][col] = x;
+                    }
+                }
             }
         if (g == 0) {
 #pragma unroll
@@ -1116,7 +1415,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // XOR-swizzled by red_swizzle of the row's head pair, which makes
         // these writes and the row-contiguous reads below conflict-free.
         {
-            const uint32_t sw = red_swizzle<kFp8, kD>(c);
+            const uint32_t sw = red_swizzle<kKv, kD>(c);
 #pragma unroll
             for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
@@ -1132,6 +1431,21 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                 make_float4(o[nb][2 * k][col], o[nb][2 * k][col + 2],
                                             o[nb][2 * k + 1][col], o[nb][2 * k + 1][col + 2]);
                         }
+                    } else if constexpr (kInt4) {
+#pragma unroll
+                        for (int gr = 0; gr < C::kGroups; ++gr)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t u = 16 * gr + 2 * g + k;
+                                const float* x = o[nb][4 * gr + 2 * k];
+                                const float* y = o[nb][4 * gr + 2 * k + 1];
+                                const float add = vbias[nb][gr][col];
+                                *reinterpret_cast<float4*>(row + 4 * (u ^ sw)) =
+                                    make_float4(fmaf(x[col] * 0x1p24f, vref, add),
+                                                fmaf(x[col + 2] * 0x1p20f, vref, add),
+                                                fmaf(y[col] * 0x1p24f, vref, add),
+                                                fmaf(y[col + 2] * 0x1p20f, vref, add));
+                            }
                     } else {
                         // m-block mb holds dims 16mb + g (col) and 16mb + g + 8 (col + 2)
 #pragma unroll
@@ -1165,7 +1479,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const int kvh = hq / G;
                 const int hl = hq - kvh * G;                 // head within its KV head's group
                 const int r0 = kvh * kWarpsPerHead * kGP + hl;   // its row in the first warp
-                const uint32_t su = u ^ red_swizzle<kFp8, kD>((hl & 7) >> 1);
+                const uint32_t su = u ^ red_swizzle<kKv, kD>((hl & 7) >> 1);
                 float M = kNegInf;
 #pragma unroll
                 for (int w = 0; w < kWarpsPerHead; ++w) M = fmaxf(M, red_m[r0 + w * kGP]);
@@ -1217,7 +1531,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         s = sn;
         have = have_next;
     }
-    if (a.cluster_size > 0) attn_cluster_reduce<kFp8, kD, kGP, kH>(a, smem);
+    if (a.cluster_size > 0) attn_cluster_reduce<kKv, kD, kGP, kH>(a, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -1276,6 +1590,7 @@ attn_merge_kernel(const AttnArgs a) {
             int nb = (len >= 1 && static_cast<int64_t>(len) <= max_tokens)
                          ? (len + kChunkTokens - 1) / kChunkTokens
                          : 0;
+            if (nb > 0 && a.window > 0) nb -= window_gap(len, a.window, a.sinks).gap;
             const int nc = nb;
             if (nb > 0 && a.chunk_begin != nullptr) nb -= a.chunk_begin[bb];
             if (bb == b) s_nc = nc;
@@ -1489,19 +1804,19 @@ attn_merge_kernel(const AttnArgs a) {
 // ---------------------------------------------------------------------------
 // host-side dispatch
 // ---------------------------------------------------------------------------
-template <bool kFp8, int kD, int kGP, int kH>
+template <int kKv, int kD, int kGP, int kH, bool kWin>
 static cudaError_t launch_variant(int grid, cudaStream_t stream, const CUtensorMap& tk,
                                   const CUtensorMap& tv, const AttnArgs& args) {
-    using C = AttnCfg<kFp8, kD, kGP, kH>;
+    using C = AttnCfg<kKv, kD, kGP, kH>;
     PdlLaunch l(dim3(grid), dim3(kAttnThreads), C::kSmemBytes, stream);
     if (args.cluster_size > 0) l.set_cluster(args.cluster_size);
-    return cudaLaunchKernelEx(&l.cfg, attn_partial_kernel<kFp8, kD, kGP, kH>, tk, tv, args);
+    return cudaLaunchKernelEx(&l.cfg, attn_partial_kernel<kKv, kD, kGP, kH, kWin>, tk, tv, args);
 }
 
-template <bool kFp8, int kD, int kGP, int kH>
+template <int kKv, int kD, int kGP, int kH, bool kWin>
 static cudaError_t max_clusters_variant(int cluster_size, int* clusters) {
-    using C = AttnCfg<kFp8, kD, kGP, kH>;
-    auto* fn = attn_partial_kernel<kFp8, kD, kGP, kH>;
+    using C = AttnCfg<kKv, kD, kGP, kH>;
+    auto* fn = attn_partial_kernel<kKv, kD, kGP, kH, kWin>;
     cudaError_t e = cudaSuccess;
     if (cluster_size > 8) {
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -1521,60 +1836,65 @@ static cudaError_t max_clusters_variant(int cluster_size, int* clusters) {
     return cudaOccupancyMaxActiveClusters(clusters, fn, &cfg);
 }
 
-// (fp8, head_dim, group pad, KV heads per item)
-#define PKV_FOR_EACH_VARIANT(X)                                                    \
-    X(true, 64, 8, 1) X(true, 64, 16, 1) X(true, 128, 8, 1) X(true, 128, 16, 1)    \
-    X(false, 64, 8, 1) X(false, 64, 16, 1) X(false, 128, 8, 1) X(false, 128, 16, 1) \
-    X(true, 64, 8, 2) X(true, 128, 8, 2)
+// (cache type, head_dim, group pad, KV heads per item), each without and
+// with a window
+#define PKV_FOR_EACH_SHAPE(X, W)                                                             \
+    X(kKvFp8, 64, 8, 1, W) X(kKvFp8, 64, 16, 1, W) X(kKvFp8, 128, 8, 1, W)                     \
+    X(kKvFp8, 128, 16, 1, W) X(kKvBf16, 64, 8, 1, W) X(kKvBf16, 64, 16, 1, W)                   \
+    X(kKvBf16, 128, 8, 1, W) X(kKvBf16, 128, 16, 1, W) X(kKvFp8, 64, 8, 2, W)                   \
+    X(kKvFp8, 128, 8, 2, W) X(kKvInt4, 64, 8, 1, W) X(kKvInt4, 64, 16, 1, W)                     \
+    X(kKvInt4, 128, 8, 1, W) X(kKvInt4, 128, 16, 1, W) X(kKvInt4, 64, 8, 2, W)                   \
+    X(kKvInt4, 128, 8, 2, W)
+#define PKV_FOR_EACH_VARIANT(X) PKV_FOR_EACH_SHAPE(X, false) PKV_FOR_EACH_SHAPE(X, true)
 
-#define PKV_MATCH(F, D, GP, H) \
-    (fp8 == F && head_dim == D && group_pad == GP && kv_per_item == H)
+#define PKV_MATCH(V, KV, D, GP, H, W)                                                   \
+    (V.kv == KV && V.head_dim == D && V.group_pad == GP && V.kv_per_item == H && V.window == W)
 
-size_t attn_partial_smem_bytes(bool fp8, int head_dim, int group_pad, int kv_per_item) {
-#define X(F, D, GP, H) \
-    if (PKV_MATCH(F, D, GP, H)) return AttnCfg<F, D, GP, H>::kSmemBytes;
+size_t attn_partial_smem_bytes(const AttnVariant& v) {
+#define X(KV, D, GP, H, W) \
+    if (PKV_MATCH(v, KV, D, GP, H, W)) return AttnCfg<KV, D, GP, H>::kSmemBytes;
     PKV_FOR_EACH_VARIANT(X)
 #undef X
     return 0;
 }
 
-cudaError_t attn_set_smem_attr(bool fp8, int head_dim, int group_pad, int kv_per_item) {
-#define X(F, D, GP, H)                                                              \
-    if (PKV_MATCH(F, D, GP, H))                                                      \
-        return cudaFuncSetAttribute(attn_partial_kernel<F, D, GP, H>,                \
+cudaError_t attn_set_smem_attr(const AttnVariant& v) {
+#define X(KV, D, GP, H, W)                                                              \
+    if (PKV_MATCH(v, KV, D, GP, H, W))                                                      \
+        return cudaFuncSetAttribute(attn_partial_kernel<KV, D, GP, H, W>,                \
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,     \
-                                    AttnCfg<F, D, GP, H>::kSmemBytes);
+                                    AttnCfg<KV, D, GP, H>::kSmemBytes);
     PKV_FOR_EACH_VARIANT(X)
 #undef X
     return cudaErrorInvalidValue;
 }
 
-cudaError_t attn_occupancy(bool fp8, int head_dim, int group_pad, int kv_per_item,
-                           int* blocks_per_sm) {
-#define X(F, D, GP, H)                                                               \
-    if (PKV_MATCH(F, D, GP, H))                                                       \
+cudaError_t attn_occupancy(const AttnVariant& v, int* blocks_per_sm) {
+#define X(KV, D, GP, H, W)                                                               \
+    if (PKV_MATCH(v, KV, D, GP, H, W))                                                       \
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(                         \
-            blocks_per_sm, attn_partial_kernel<F, D, GP, H>, kAttnThreads,            \
-            AttnCfg<F, D, GP, H>::kSmemBytes);
+            blocks_per_sm, attn_partial_kernel<KV, D, GP, H, W>, kAttnThreads,            \
+            AttnCfg<KV, D, GP, H>::kSmemBytes);
     PKV_FOR_EACH_VARIANT(X)
 #undef X
     return cudaErrorInvalidValue;
 }
 
-cudaError_t attn_max_clusters(bool fp8, int head_dim, int group_pad, int kv_per_item,
-                              int cluster_size, int* clusters) {
-#define X(F, D, GP, H) \
-    if (PKV_MATCH(F, D, GP, H)) return max_clusters_variant<F, D, GP, H>(cluster_size, clusters);
+cudaError_t attn_max_clusters(const AttnVariant& v, int cluster_size, int* clusters) {
+#define X(KV, D, GP, H, W) \
+    if (PKV_MATCH(v, KV, D, GP, H, W))      \
+        return max_clusters_variant<KV, D, GP, H, W>(cluster_size, clusters);
     PKV_FOR_EACH_VARIANT(X)
 #undef X
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_attn_partial(bool fp8, int head_dim, int group_pad, int kv_per_item, int grid,
-                                cudaStream_t stream, const CUtensorMap& tmap_k,
-                                const CUtensorMap& tmap_v, const AttnArgs& args) {
-#define X(F, D, GP, H) \
-    if (PKV_MATCH(F, D, GP, H)) return launch_variant<F, D, GP, H>(grid, stream, tmap_k, tmap_v, args);
+cudaError_t launch_attn_partial(const AttnVariant& v, int grid, cudaStream_t stream,
+                                const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
+                                const AttnArgs& args) {
+#define X(KV, D, GP, H, W) \
+    if (PKV_MATCH(v, KV, D, GP, H, W))      \
+        return launch_variant<KV, D, GP, H, W>(grid, stream, tmap_k, tmap_v, args);
     PKV_FOR_EACH_VARIANT(X)
 #undef X
     return cudaErrorInvalidValue;

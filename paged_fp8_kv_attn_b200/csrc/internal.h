@@ -14,6 +14,13 @@ constexpr int kChunkTokens = 64;
 // the non-portable maximum on sm_100).
 constexpr int kMaxCluster = 16;
 
+// Cache types (the values of PKV_KV_*), and the dims that share a (scale,
+// minimum) pair in an INT4 cache.
+constexpr int kKvFp8 = 0;
+constexpr int kKvBf16 = 1;
+constexpr int kKvInt4 = 2;
+constexpr int kInt4Group = 64;
+
 // Arguments of the split-K partial and merge kernels (passed by value).
 struct AttnArgs {
     const uint16_t* q;          // [B][Hq][D] bf16
@@ -49,6 +56,12 @@ struct AttnArgs {
     const int32_t* chunk_begin;  // [B]
     const float* pfx_ml;         // [items][G][4]
     const float* pfx_o;          // [items][G][D]
+    // INT4: the pools' (scale, minimum) pairs, [NP][Hkv][P][D/64][2] bf16.
+    const uint8_t* k_params;
+    const uint8_t* v_params;
+    // Window: tokens t < sinks and t >= len - window are visible (window 0: all).
+    int32_t window;
+    int32_t sinks;
 };
 
 // Shared-prefix pass (prefix.cu): FP8, head_dim 128, two KV heads per item.
@@ -107,10 +120,10 @@ cudaError_t launch_prefix_attn(int grid, cudaStream_t stream, const CUtensorMap&
 void set_last_error(const char* message);
 
 // KV heads one attention work item covers: two adjacent heads (one
-// contiguous 16 KiB K or V block per 64-token page) for FP8 caches with an
-// even number of KV heads and a GQA group of at most 8; otherwise one.
-inline int kv_heads_per_item(bool fp8, int num_kv_heads, int group) {
-    return (fp8 && num_kv_heads % 2 == 0 && group <= 8) ? 2 : 1;
+// contiguous 16 KiB K or V block per 64-token page) for FP8 and INT4 caches
+// with an even number of KV heads and a GQA group of at most 8; otherwise one.
+inline int kv_heads_per_item(int kv, int num_kv_heads, int group) {
+    return (kv != kKvBf16 && num_kv_heads % 2 == 0 && group <= 8) ? 2 : 1;
 }
 
 // Workspace layout for given sizes and grid (slots = grid + work items).
@@ -120,44 +133,61 @@ struct WorkspaceLayout {
 WorkspaceLayout workspace_layout(int32_t batch, int32_t group, int32_t num_kv_heads,
                                  int32_t kv_per_item, int32_t head_dim, int32_t num_ctas);
 
+// One compiled variant of the attention kernel.
+struct AttnVariant {
+    int kv;            // kKvFp8, kKvBf16 or kKvInt4
+    int head_dim;
+    int group_pad;     // 8 or 16
+    int kv_per_item;   // KV heads per work item
+    bool window;
+};
+
 // Attention variant properties: dynamic shared memory bytes.  Returns 0 if
 // the combination is not compiled.
-size_t attn_partial_smem_bytes(bool fp8, int head_dim, int group_pad, int kv_per_item);
-cudaError_t attn_set_smem_attr(bool fp8, int head_dim, int group_pad, int kv_per_item);
-cudaError_t attn_occupancy(bool fp8, int head_dim, int group_pad, int kv_per_item,
-                           int* blocks_per_sm);
+size_t attn_partial_smem_bytes(const AttnVariant& v);
+cudaError_t attn_set_smem_attr(const AttnVariant& v);
+cudaError_t attn_occupancy(const AttnVariant& v, int* blocks_per_sm);
 constexpr int kAttnThreads = 160;   // 4 consumer warps + 1 producer warp
 
 // Clusters of `cluster_size` CTAs that can be resident at once (0 if none).
-cudaError_t attn_max_clusters(bool fp8, int head_dim, int group_pad, int kv_per_item,
-                              int cluster_size, int* clusters);
+cudaError_t attn_max_clusters(const AttnVariant& v, int cluster_size, int* clusters);
 // grid CTAs; with args.cluster_size > 0 launched as clusters of that size.
-cudaError_t launch_attn_partial(bool fp8, int head_dim, int group_pad, int kv_per_item, int grid,
-                                cudaStream_t stream, const CUtensorMap& tmap_k,
-                                const CUtensorMap& tmap_v, const AttnArgs& args);
+cudaError_t launch_attn_partial(const AttnVariant& v, int grid, cudaStream_t stream,
+                                const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
+                                const AttnArgs& args);
 cudaError_t launch_attn_merge(int head_dim, cudaStream_t stream, const AttnArgs& args);
 
+// window > 0: only the pages holding one of the last `window` or the first
+// `sinks` tokens are checked.
 cudaError_t launch_tag_check(const uint32_t* page_tags, int32_t num_pages,
                              const int32_t* page_table, const uint32_t* expected_tags,
                              int32_t max_pages, const int32_t* seq_lens, int32_t batch,
-                             int32_t page_size, uint8_t* abort_out, int32_t* num_aborted,
-                             cudaStream_t stream);
+                             int32_t page_size, int32_t window, int32_t sinks, uint8_t* abort_out,
+                             int32_t* num_aborted, cudaStream_t stream);
 
-cudaError_t launch_append(bool fp8, const uint16_t* k_new, const uint16_t* v_new,
+// The K and V pools a kernel writes.
+struct KvDst {
+    int kv;                 // kKvFp8, kKvBf16 or kKvInt4
+    void* k;
+    void* v;
+    float k_scale, v_scale;   // FP8
+    uint32_t* k_params;       // INT4: (scale, minimum) pairs
+    uint32_t* v_params;
+};
+
+cudaError_t launch_append(const KvDst& dst, const uint16_t* k_new, const uint16_t* v_new,
                           const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
                           int32_t batch, int32_t num_kv_heads, int32_t head_dim,
-                          int32_t page_size, float k_scale, float v_scale, void* k_cache,
-                          void* v_cache, int32_t num_pages, const uint8_t* abort,
+                          int32_t page_size, int32_t num_pages, const uint8_t* abort,
                           cudaStream_t stream);
 
 // all of the SM's on-chip memory as shared memory for the step's first kernels
 cudaError_t step_kernels_set_carveout();
-cudaError_t launch_check_append(bool fp8, const uint32_t* page_tags, int32_t num_pages,
+cudaError_t launch_check_append(const KvDst& dst, const uint32_t* page_tags, int32_t num_pages,
                                 const int32_t* page_table, const uint32_t* expected_tags,
                                 int32_t max_pages, const int32_t* seq_lens, int32_t batch,
                                 int32_t page_size, const uint16_t* k_new, const uint16_t* v_new,
-                                int32_t num_kv_heads, int32_t head_dim, float k_scale,
-                                float v_scale, void* k_cache, void* v_cache, uint8_t* abort_out,
+                                int32_t num_kv_heads, int32_t head_dim, uint8_t* abort_out,
                                 int32_t* num_aborted, cudaStream_t stream);
 
 cudaError_t launch_retag(uint32_t* page_tags, int32_t num_pages, const int32_t* pages, int32_t n,
@@ -171,6 +201,50 @@ cudaError_t launch_requant(const uint16_t* src_pool, int32_t src_num_pages,
                            const int32_t* src_pages, uint8_t* dst_pool, int32_t dst_num_pages,
                            const int32_t* dst_pages, int32_t num_pairs, int64_t page_elems,
                            float scale, cudaStream_t stream);
+
+cudaError_t launch_requant_int4(const uint16_t* src_pool, int32_t src_num_pages,
+                                const int32_t* src_pages, uint8_t* dst_codes,
+                                uint32_t* dst_params, int32_t dst_num_pages,
+                                const int32_t* dst_pages, int32_t num_pairs, int64_t page_elems,
+                                int32_t head_dim, cudaStream_t stream);
+
+// Token writes into cache slots and reads back (kv_slots.cu): token i's row is
+// k + i * k_stride elements, its slot slot_map[i] = page * P + offset.
+struct SlotArgs {
+    const int32_t* slot_map;   // [num_tokens]; outside [0, num_pages * P): no slot
+    int32_t num_tokens;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t num_pages;
+    int64_t k_stride, v_stride;
+};
+cudaError_t launch_write_slots(const KvDst& dst, const uint16_t* k_new, const uint16_t* v_new,
+                               const SlotArgs& args, cudaStream_t stream);
+cudaError_t launch_read_slots(const KvDst& src, uint16_t* k_out, uint16_t* v_out,
+                              const SlotArgs& args, cudaStream_t stream);
+
+// Page tables and slot maps from request lengths (kv_tables.cu).
+struct TableArgs {
+    const int32_t* old_lens;     // [batch]
+    const int32_t* new_lens;     // [batch]
+    const int32_t* free_pages;   // [free_capacity], top of the stack at *num_free - 1
+    const int32_t* num_free;     // [1]
+    int32_t* num_free_out;       // [1], may be num_free
+    int32_t* page_table;         // [batch][max_pages]
+    const uint32_t* page_tags;   // [num_pages] or null
+    uint32_t* expected_tags;     // [batch][max_pages] or null
+    int32_t* cu_tokens;          // [batch + 1]
+    int32_t* slot_map;           // [max_tokens]
+    uint8_t* failed;             // [batch]
+    int32_t batch;
+    int32_t page_size;
+    int32_t free_capacity;
+    int32_t num_pages;
+    int32_t max_pages;
+    int32_t max_tokens;
+};
+cudaError_t launch_extend_tables(const TableArgs& args, cudaStream_t stream);
 
 // INT4 weight dequantisation GEMV: CTA tile (weight rows), k-tile (columns
 // per pipeline stage), scale group and largest batch.

@@ -9,6 +9,7 @@
 // into the attention kernel).
 #include "device.cuh"
 #include "internal.h"
+#include "kv_codec.cuh"
 
 namespace pkv {
 
@@ -21,8 +22,9 @@ __global__ void __launch_bounds__(kTagThreads)
 tag_check_kernel(const uint32_t* __restrict__ page_tags, int32_t num_pages,
                  const int32_t* __restrict__ page_table,
                  const uint32_t* __restrict__ expected_tags, int32_t max_pages,
-                 const int32_t* __restrict__ seq_lens, int32_t page_size,
-                 uint8_t* __restrict__ abort_out, int32_t* __restrict__ num_aborted) {
+                 const int32_t* __restrict__ seq_lens, int32_t page_size, int32_t window,
+                 int32_t sinks, uint8_t* __restrict__ abort_out,
+                 int32_t* __restrict__ num_aborted) {
     // Let the next kernel on the stream launch at once (its own prologue
     // overlaps this grid); it still waits for this grid to finish before it
     // reads anything this grid writes.
@@ -32,11 +34,20 @@ tag_check_kernel(const uint32_t* __restrict__ page_tags, int32_t num_pages,
     const int32_t L = seq_lens[b];
     int bad = (L < 1 || static_cast<int64_t>(L) > static_cast<int64_t>(max_pages) * page_size);
     if (!bad) {
-        const int32_t used = (L + page_size - 1) / page_size;
+        // (window > 0: entries [skip, skip + gap) hold hidden tokens only)
+        int32_t used = (L + page_size - 1) / page_size, skip = used, gap = 0;
+        if (window > 0) {
+            const int32_t lo = L > window ? L - window : 0;
+            const int32_t s = sinks < lo ? sinks : lo;
+            skip = (s + page_size - 1) / page_size;
+            gap = lo / page_size > skip ? lo / page_size - skip : 0;
+            used -= gap;
+        }
         const int32_t* row = page_table + static_cast<int64_t>(b) * max_pages;
         const uint32_t* exp = expected_tags + static_cast<int64_t>(b) * max_pages;
 #pragma unroll 4
-        for (int j = threadIdx.x; j < used; j += kTagThreads) {
+        for (int i = threadIdx.x; i < used; i += kTagThreads) {
+            const int j = i < skip ? i : i + gap;
             const int32_t pid = row[j];
             const uint32_t want = exp[j];
             if (pid < 0 || pid >= num_pages)
@@ -55,37 +66,12 @@ tag_check_kernel(const uint32_t* __restrict__ page_tags, int32_t num_pages,
 cudaError_t launch_tag_check(const uint32_t* page_tags, int32_t num_pages,
                              const int32_t* page_table, const uint32_t* expected_tags,
                              int32_t max_pages, const int32_t* seq_lens, int32_t batch,
-                             int32_t page_size, uint8_t* abort_out, int32_t* num_aborted,
-                             cudaStream_t stream) {
+                             int32_t page_size, int32_t window, int32_t sinks, uint8_t* abort_out,
+                             int32_t* num_aborted, cudaStream_t stream) {
     PdlLaunch l(dim3(batch), dim3(kTagThreads), 0, stream);
     return cudaLaunchKernelEx(&l.cfg, tag_check_kernel, page_tags, num_pages, page_table,
-                              expected_tags, max_pages, seq_lens, page_size, abort_out,
-                              num_aborted);
-}
-
-// ---------------------------------------------------------------------------
-// E4M3 quantisation of bf16 values: y = x / scale as one correctly rounded
-// binary32 division, then the hardware's round-to-nearest-even conversion
-// with saturation to +-448; a NaN input becomes S.1111.111 with its sign.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t quantize_pair(float x_lo, float x_hi, float scale) {
-    const float y_lo = __fdiv_rn(x_lo, scale);
-    const float y_hi = __fdiv_rn(x_hi, scale);
-    uint32_t p = f32x2_to_e4m3x2(y_hi, y_lo);
-    // The quotient of a NaN is a NaN of unspecified sign; the code takes the
-    // sign of the input (a finite, positive scale makes y NaN iff x is).
-    if (isnan(x_lo)) p = (p & 0xFF00u) | (signbit(x_lo) ? 0xFFu : 0x7Fu);
-    if (isnan(x_hi)) p = (p & 0x00FFu) | ((signbit(x_hi) ? 0xFFu : 0x7Fu) << 8);
-    return p;
-}
-// 8 bf16 values (one 16-byte word) -> 8 codes (two 32-bit words).
-__device__ __forceinline__ uint2 quantize8(uint4 raw, float scale) {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t p[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        p[i] = quantize_pair(bf16_bits_to_f32(w[i] & 0xFFFFu), bf16_bits_to_f32(w[i] >> 16), scale);
-    return make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
+                              expected_tags, max_pages, seq_lens, page_size, window, sinks,
+                              abort_out, num_aborted);
 }
 
 // ---------------------------------------------------------------------------
@@ -93,13 +79,15 @@ __device__ __forceinline__ uint2 quantize8(uint4 raw, float scale) {
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 
-template <bool kFp8>
+template <int kKv>
 __global__ void __launch_bounds__(kAppendThreads)
 append_kernel(const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new,
               const int32_t* __restrict__ page_table, int32_t max_pages,
               const int32_t* __restrict__ seq_lens, int32_t num_kv_heads, int32_t head_dim,
               int32_t page_size, float k_scale, float v_scale, void* __restrict__ k_cache,
-              void* __restrict__ v_cache, int32_t num_pages, const uint8_t* __restrict__ abort) {
+              void* __restrict__ v_cache, uint32_t* __restrict__ k_params,
+              uint32_t* __restrict__ v_params, int32_t num_pages,
+              const uint8_t* __restrict__ abort) {
     // Let the next kernel on the stream launch at once (its own prologue
     // overlaps this grid); it still waits for this grid to finish before it
     // reads anything this grid writes.
@@ -122,32 +110,24 @@ append_kernel(const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v
         const uint16_t* src = (is_v ? v_new : k_new) +
                               (static_cast<int64_t>(b) * num_kv_heads + h) * head_dim + d8 * 8;
         const uint4 raw = *reinterpret_cast<const uint4*>(src);
-        const int64_t dst =
-            ((static_cast<int64_t>(pid) * num_kv_heads + h) * page_size + slot) * head_dim + d8 * 8;
-        if constexpr (kFp8) {
-            uint8_t* cache = static_cast<uint8_t*>(is_v ? v_cache : k_cache);
-            *reinterpret_cast<uint2*>(cache + dst) = quantize8(raw, is_v ? v_scale : k_scale);
-        } else {
-            uint16_t* cache = static_cast<uint16_t*>(is_v ? v_cache : k_cache);
-            *reinterpret_cast<uint4*>(cache + dst) = raw;
-        }
+        const int64_t dst = (static_cast<int64_t>(pid) * num_kv_heads + h) * page_size + slot;
+        store8<kKv>(is_v ? v_cache : k_cache, is_v ? v_params : k_params, dst, head_dim, d8, raw,
+                    is_v ? v_scale : k_scale);
     }
 }
 
-cudaError_t launch_append(bool fp8, const uint16_t* k_new, const uint16_t* v_new,
+cudaError_t launch_append(const KvDst& dst, const uint16_t* k_new, const uint16_t* v_new,
                           const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
                           int32_t batch, int32_t num_kv_heads, int32_t head_dim,
-                          int32_t page_size, float k_scale, float v_scale, void* k_cache,
-                          void* v_cache, int32_t num_pages, const uint8_t* abort,
+                          int32_t page_size, int32_t num_pages, const uint8_t* abort,
                           cudaStream_t stream) {
     PdlLaunch l(dim3(batch), dim3(kAppendThreads), 0, stream);
-    if (fp8)
-        return cudaLaunchKernelEx(&l.cfg, append_kernel<true>, k_new, v_new, page_table,
-                                  max_pages, seq_lens, num_kv_heads, head_dim, page_size, k_scale,
-                                  v_scale, k_cache, v_cache, num_pages, abort);
-    return cudaLaunchKernelEx(&l.cfg, append_kernel<false>, k_new, v_new, page_table, max_pages,
-                              seq_lens, num_kv_heads, head_dim, page_size, k_scale, v_scale,
-                              k_cache, v_cache, num_pages, abort);
+    auto* kernel = dst.kv == kKvFp8    ? append_kernel<kKvFp8>
+                   : dst.kv == kKvBf16 ? append_kernel<kKvBf16>
+                                       : append_kernel<kKvInt4>;
+    return cudaLaunchKernelEx(&l.cfg, kernel, k_new, v_new, page_table, max_pages, seq_lens,
+                              num_kv_heads, head_dim, page_size, dst.k_scale, dst.v_scale, dst.k,
+                              dst.v, dst.k_params, dst.v_params, num_pages, abort);
 }
 
 // ---------------------------------------------------------------------------
@@ -159,7 +139,7 @@ cudaError_t launch_append(bool fp8, const uint16_t* k_new, const uint16_t* v_new
 // ---------------------------------------------------------------------------
 constexpr int kFusedThreads = 256;
 
-template <bool kFp8>
+template <int kKv>
 __global__ void __launch_bounds__(kFusedThreads)
 check_append_kernel(const uint32_t* __restrict__ page_tags, int32_t num_pages,
                     const int32_t* __restrict__ page_table,
@@ -168,6 +148,7 @@ check_append_kernel(const uint32_t* __restrict__ page_tags, int32_t num_pages,
                     const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new,
                     int32_t num_kv_heads, int32_t head_dim, float k_scale, float v_scale,
                     void* __restrict__ k_cache, void* __restrict__ v_cache,
+                    uint32_t* __restrict__ k_params, uint32_t* __restrict__ v_params,
                     uint8_t* __restrict__ abort_out, int32_t* __restrict__ num_aborted) {
     launch_dependents();
     grid_dependency_wait();
@@ -231,34 +212,25 @@ check_append_kernel(const uint32_t* __restrict__ page_tags, int32_t num_pages,
             val = *reinterpret_cast<const uint4*>(
                 (is_v ? v_new : k_new) + (static_cast<int64_t>(b) * num_kv_heads + h) * head_dim +
                 d8 * 8);
-        const int64_t dst =
-            ((static_cast<int64_t>(pid) * num_kv_heads + h) * page_size + slot) * head_dim + d8 * 8;
-        if constexpr (kFp8) {
-            uint8_t* cache = static_cast<uint8_t*>(is_v ? v_cache : k_cache);
-            *reinterpret_cast<uint2*>(cache + dst) = quantize8(val, is_v ? v_scale : k_scale);
-        } else {
-            uint16_t* cache = static_cast<uint16_t*>(is_v ? v_cache : k_cache);
-            *reinterpret_cast<uint4*>(cache + dst) = val;
-        }
+        const int64_t dst = (static_cast<int64_t>(pid) * num_kv_heads + h) * page_size + slot;
+        store8<kKv>(is_v ? v_cache : k_cache, is_v ? v_params : k_params, dst, head_dim, d8, val,
+                    is_v ? v_scale : k_scale);
     }
 }
 
-cudaError_t launch_check_append(bool fp8, const uint32_t* page_tags, int32_t num_pages,
+cudaError_t launch_check_append(const KvDst& dst, const uint32_t* page_tags, int32_t num_pages,
                                 const int32_t* page_table, const uint32_t* expected_tags,
                                 int32_t max_pages, const int32_t* seq_lens, int32_t batch,
                                 int32_t page_size, const uint16_t* k_new, const uint16_t* v_new,
-                                int32_t num_kv_heads, int32_t head_dim, float k_scale,
-                                float v_scale, void* k_cache, void* v_cache, uint8_t* abort_out,
+                                int32_t num_kv_heads, int32_t head_dim, uint8_t* abort_out,
                                 int32_t* num_aborted, cudaStream_t stream) {
     PdlLaunch l(dim3(batch), dim3(kFusedThreads), 0, stream);
-    if (fp8)
-        return cudaLaunchKernelEx(&l.cfg, check_append_kernel<true>, page_tags, num_pages,
-                                  page_table, expected_tags, max_pages, seq_lens, page_size, k_new,
-                                  v_new, num_kv_heads, head_dim, k_scale, v_scale, k_cache, v_cache,
-                                  abort_out, num_aborted);
-    return cudaLaunchKernelEx(&l.cfg, check_append_kernel<false>, page_tags, num_pages, page_table,
-                              expected_tags, max_pages, seq_lens, page_size, k_new, v_new,
-                              num_kv_heads, head_dim, k_scale, v_scale, k_cache, v_cache,
+    auto* kernel = dst.kv == kKvFp8    ? check_append_kernel<kKvFp8>
+                   : dst.kv == kKvBf16 ? check_append_kernel<kKvBf16>
+                                       : check_append_kernel<kKvInt4>;
+    return cudaLaunchKernelEx(&l.cfg, kernel, page_tags, num_pages, page_table, expected_tags,
+                              max_pages, seq_lens, page_size, k_new, v_new, num_kv_heads, head_dim,
+                              dst.k_scale, dst.v_scale, dst.k, dst.v, dst.k_params, dst.v_params,
                               abort_out, num_aborted);
 }
 
@@ -347,18 +319,58 @@ requant_kernel(const uint16_t* __restrict__ src_pool, int32_t src_num_pages,
     }
 }
 
+// INT4: 8 values a thread, a group of 64 in 8 consecutive lanes (page_elems is
+// a multiple of 64, so a group never spans two pairs or the end).
+__global__ void __launch_bounds__(kRequantThreads)
+requant_int4_kernel(const uint16_t* __restrict__ src_pool, int32_t src_num_pages,
+                    const int32_t* __restrict__ src_pages, uint8_t* __restrict__ dst_codes,
+                    uint32_t* __restrict__ dst_params, int32_t dst_num_pages,
+                    const int32_t* __restrict__ dst_pages, int32_t num_pairs, int64_t page_elems,
+                    int32_t head_dim) {
+    launch_dependents();
+    grid_dependency_wait();
+    const int64_t blocks = page_elems / 8;
+    const int64_t total = static_cast<int64_t>(num_pairs) * blocks;
+    const int per_row = head_dim / 8;
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int32_t pair = static_cast<int32_t>(i / blocks);
+        const int64_t bi = i % blocks;
+        const int32_t s = src_pages[pair];
+        const int32_t d = dst_pages[pair];
+        if (s < 0 || s >= src_num_pages || d < 0 || d >= dst_num_pages) continue;
+        const uint4 raw = *reinterpret_cast<const uint4*>(src_pool + s * page_elems + bi * 8);
+        store8<kKvInt4>(dst_codes, dst_params, (d * page_elems) / head_dim + bi / per_row, head_dim,
+                        static_cast<int>(bi % per_row), raw, 1.f);
+    }
+}
+
+static int64_t requant_blocks(int64_t threads) {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int64_t blocks = (threads + kRequantThreads - 1) / kRequantThreads;
+    const int64_t cap = static_cast<int64_t>(sms) * 8;
+    return blocks > cap ? cap : (blocks < 1 ? 1 : blocks);
+}
+
+cudaError_t launch_requant_int4(const uint16_t* src_pool, int32_t src_num_pages,
+                                const int32_t* src_pages, uint8_t* dst_codes,
+                                uint32_t* dst_params, int32_t dst_num_pages,
+                                const int32_t* dst_pages, int32_t num_pairs, int64_t page_elems,
+                                int32_t head_dim, cudaStream_t stream) {
+    const int64_t blocks = requant_blocks(static_cast<int64_t>(num_pairs) * (page_elems / 8));
+    PdlLaunch l(dim3(static_cast<unsigned>(blocks)), dim3(kRequantThreads), 0, stream);
+    return cudaLaunchKernelEx(&l.cfg, requant_int4_kernel, src_pool, src_num_pages, src_pages,
+                              dst_codes, dst_params, dst_num_pages, dst_pages, num_pairs,
+                              page_elems, head_dim);
+}
+
 cudaError_t launch_requant(const uint16_t* src_pool, int32_t src_num_pages,
                            const int32_t* src_pages, uint8_t* dst_pool, int32_t dst_num_pages,
                            const int32_t* dst_pages, int32_t num_pairs, int64_t page_elems,
                            float scale, cudaStream_t stream) {
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t total = static_cast<int64_t>(num_pairs) * (page_elems / 16);
-    int64_t blocks = (total + kRequantThreads - 1) / kRequantThreads;
-    const int64_t cap = static_cast<int64_t>(sms) * 8;
-    if (blocks > cap) blocks = cap;
-    if (blocks < 1) blocks = 1;
+    const int64_t blocks = requant_blocks(static_cast<int64_t>(num_pairs) * (page_elems / 16));
     PdlLaunch l(dim3(static_cast<unsigned>(blocks)), dim3(kRequantThreads), 0, stream);
     return cudaLaunchKernelEx(&l.cfg, requant_kernel, src_pool, src_num_pages, src_pages,
                               dst_pool, dst_num_pages, dst_pages, num_pairs, page_elems, scale);
@@ -372,10 +384,12 @@ cudaError_t step_kernels_set_carveout() {
     const int c = cudaSharedmemCarveoutMaxShared;
     const cudaFuncAttribute at = cudaFuncAttributePreferredSharedMemoryCarveout;
     cudaError_t e = cudaFuncSetAttribute(tag_check_kernel, at, c);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(append_kernel<true>, at, c);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(append_kernel<false>, at, c);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(check_append_kernel<true>, at, c);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(check_append_kernel<false>, at, c);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(append_kernel<kKvFp8>, at, c);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(append_kernel<kKvBf16>, at, c);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(append_kernel<kKvInt4>, at, c);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(check_append_kernel<kKvFp8>, at, c);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(check_append_kernel<kKvBf16>, at, c);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(check_append_kernel<kKvInt4>, at, c);
     return e;
 }
 
