@@ -150,15 +150,23 @@ def _check(name: str, status: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# (the handle alone: torch.cuda.current_stream() builds an object, 3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _need(t, dtype, ndim, name):
+    # (one line of cheap tests for the usual case: a call's host time is mostly these)
+    if t is not None and t.is_cuda and t.dim() == ndim and t.is_contiguous() and (
+            t.dtype is dtype or type(dtype) is tuple and t.dtype in dtype):
+        return t
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
@@ -167,13 +175,19 @@ def _need(t, dtype, ndim, name):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _vector(t, n, dtype, name):
+    """Address of a vector of n entries."""
+    _need(t, dtype, 1, name)
+    if t.numel() != n:
+        raise ValueError(f"{name} must be ({n},), got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _match(name, t, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -188,13 +202,13 @@ def _here(stream, *tensors):
 def _int4_pools(k_codes, k_params, v_codes, v_params):
     """(NP, Hkv, P, D) of an INT4 cache."""
     _need(k_codes, torch.uint8, 4, "k_codes")
-    NP, Hkv, P, half = k_codes.shape
-    D = 2 * half
-    _match("v_codes", _need(v_codes, torch.uint8, 4, "v_codes"), k_codes.shape)
-    par = (NP, Hkv, P, D // INT4_GROUP, 2)
+    shape = k_codes.shape
+    NP, Hkv, P, half = shape
+    par = (NP, Hkv, P, 2 * half // INT4_GROUP, 2)
+    _match("v_codes", _need(v_codes, torch.uint8, 4, "v_codes"), shape)
     _match("k_params", _need(k_params, torch.bfloat16, 5, "k_params"), par)
     _match("v_params", _need(v_params, torch.bfloat16, 5, "v_params"), par)
-    return NP, Hkv, P, D
+    return NP, Hkv, P, 2 * half
 
 
 def _pools(k_cache, v_cache, dtype):
@@ -398,26 +412,27 @@ def _token_rows(t, name, T, Hkv, D):
     """Row stride of [T][Hkv][D] token rows, each row contiguous."""
     if t is None or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
     _match(name, t, (T, Hkv, D))
-    if T == 0:
-        return Hkv * D
-    if t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != D) or (T > 1 and t.stride(0) < Hkv * D):
+    row, stride = Hkv * D, t.stride()
+    if T < 2:
+        stride = (row, *stride[1:])
+    if T and (stride[2] != 1 or (Hkv > 1 and stride[1] != D) or stride[0] < row):
         raise ValueError(f"{name} must hold each token's [Hkv][D] values contiguously")
-    return t.stride(0) if T > 1 else Hkv * D
+    return stride[0]
 
 
 def _slot_call(name, slot_map, pools, scales, k, v, shape, write, stream):
-    _need(slot_map, torch.int32, 1, "slot_map")
-    T = slot_map.shape[0]
+    T = _need(slot_map, torch.int32, 1, "slot_map").numel()
     NP, Hkv, P, D = shape
     ks, vs = _token_rows(k, "k", T, Hkv, D), _token_rows(v, "v", T, Hkv, D)
     _here(stream, slot_map, *pools, k, v)
-    mid = (_ptr(slot_map), T, Hkv, D, P, *scales, *map(_ptr, pools), NP)
-    rows, strides = (_ptr(k), _ptr(v)), (ks, vs)
-    args = (*rows, *strides, *mid) if write else (*mid, *rows, *strides)
-    _check(name, getattr(_load(), name)(*args, _stream(stream)))
+    rows = (k.data_ptr(), v.data_ptr(), ks, vs)
+    cache = (slot_map.data_ptr(), T, Hkv, D, P, *scales, *[t.data_ptr() for t in pools], NP)
+    fn = getattr(_load(), name)
+    _check(name, fn(*rows, *cache, _stream(stream)) if write else
+           fn(*cache, *rows, _stream(stream)))
 
 
 def kv_write_slots_fp8(k_new, v_new, slot_map, k_scale, v_scale, k_cache, v_cache, stream=None):
@@ -465,28 +480,24 @@ def kv_extend_tables(old_lens, new_lens, page_size, free_pages, num_free, page_t
     free stack into page_table (and their tags into expected_tags), and write the new
     tokens' slots, their packed offsets cu_tokens, the failed flags and num_free_out
     (which may be num_free)."""
-    for name, t in (("old_lens", old_lens), ("new_lens", new_lens), ("free_pages", free_pages),
-                    ("num_free", num_free), ("slot_map", slot_map), ("cu_tokens", cu_tokens),
-                    ("num_free_out", num_free_out)):
-        _need(t, torch.int32, 1, name)
-    B, MP = _need(page_table, torch.int32, 2, "page_table").shape
-    _need(failed, torch.uint8, 1, "failed")
-    for name, t, n in (("old_lens", old_lens, B), ("new_lens", new_lens, B), ("failed", failed, B),
-                       ("cu_tokens", cu_tokens, B + 1), ("num_free", num_free, 1),
-                       ("num_free_out", num_free_out, 1)):
-        _match(name, t, (n,))
-    if (page_tags is None) != (expected_tags is None):
-        raise ValueError("page_tags and expected_tags are given together or not at all")
-    if page_tags is not None:
-        _match("page_tags", _need(page_tags, _TAG_DTYPES, 1, "page_tags"), (num_pages,))
+    i32 = torch.int32
+    B, MP = _need(page_table, i32, 2, "page_table").shape
+    tags = expected = None
+    if page_tags is not None or expected_tags is not None:
+        if page_tags is None or expected_tags is None:
+            raise ValueError("page_tags and expected_tags are given together or not at all")
+        tags = _vector(page_tags, num_pages, _TAG_DTYPES, "page_tags")
         _match("expected_tags", _need(expected_tags, _TAG_DTYPES, 2, "expected_tags"), (B, MP))
+        expected = expected_tags.data_ptr()
+    T, cap = _need(slot_map, i32, 1, "slot_map").numel(), _need(free_pages, i32, 1, "free_pages").numel()
+    args = (_vector(old_lens, B, i32, "old_lens"), _vector(new_lens, B, i32, "new_lens"), B,
+            int(page_size), free_pages.data_ptr(), cap, _vector(num_free, 1, i32, "num_free"),
+            _vector(num_free_out, 1, i32, "num_free_out"), int(num_pages), page_table.data_ptr(), MP,
+            tags, expected, slot_map.data_ptr(), T, _vector(cu_tokens, B + 1, i32, "cu_tokens"),
+            _vector(failed, B, torch.uint8, "failed"))
     _here(stream, old_lens, new_lens, free_pages, num_free, num_free_out, page_table, page_tags,
           expected_tags, slot_map, cu_tokens, failed)
-    _check("kv_extend_tables", _load().kv_extend_tables(
-        _ptr(old_lens), _ptr(new_lens), B, int(page_size), _ptr(free_pages), free_pages.shape[0],
-        _ptr(num_free), _ptr(num_free_out), int(num_pages), _ptr(page_table), MP, _ptr(page_tags),
-        _ptr(expected_tags), _ptr(slot_map), slot_map.shape[0], _ptr(cu_tokens), _ptr(failed),
-        _stream(stream)))
+    _check("kv_extend_tables", _load().kv_extend_tables(*args, _stream(stream)))
 
 
 def kv_requant_pages_fp8(src_pool, src_pages, dst_pool, dst_pages, scale, stream=None):

@@ -72,10 +72,10 @@ struct AttnCfg {
     // resident warps matter more than depth (each CTA keeps up to kStages
     // chunks in flight), so the depth is the largest that still lets
     // kMinBlocks CTAs share an SM's 228 KB of shared memory.
-    static constexpr int kStages = kInt4 ? (kD == 128 ? (kH == 2 ? 5 : 6) : 8)
+    static constexpr int kStages = kInt4 ? (kD == 128 ? (kH == 2 ? 3 : 6) : 6)
                                    : kFp8 ? (kD == 128 ? (kH == 2 ? 3 : 4) : (kH == 2 ? 3 : 6))
                                           : (kD == 128 ? 2 : 4);
-    static constexpr int kMinBlocks = (kFp8 && kGP == 8 && kH == 1) ? 3 : 2;
+    static constexpr int kMinBlocks = (kFp8 && kGP == 8 && kH == 1) || (kInt4 && kGP == 8) ? 3 : 2;
     // The epilogue's cross-warp reduction of O (4 warps x kGP heads x kD fp32)
     // reuses the stage of the segment's last chunk when it fits there (a
     // group of 8: exactly one FP8 stage), which is released to the producer
@@ -116,28 +116,19 @@ struct AttnCfg {
 // per accumulator layout so that one store instruction's lanes (and each
 // 8-lane phase of a 16-byte store) reach distinct banks: FP8 D=128 stores
 // units 4g+k, FP8 D=64 units 2g+k, BF16 single words of units 4mb+g/4 (+2).
-// INT4 stores units 16 group + 2g+k: the pattern of FP8 D=64 at both sizes.
+// INT4 stores units 16 group + 8 half + g.
 template <int kKv, int kD>
 __device__ __forceinline__ uint32_t red_swizzle(int c) {
-    if constexpr (kKv == kKvBf16) return 2u * c;
+    if constexpr (kKv != kKvFp8) return 2u * c;
     else if constexpr (kKv == kKvFp8 && kD == 128) return static_cast<uint32_t>(c);
     else return static_cast<uint32_t>((c & 1) | ((c & 2) << 1));
 }
 
 // Token permutation inside an 8-row group: row tau(n) feeds MMA column n.
-// INT4 rows are 64 (D = 128, 64-byte swizzle) or 32 bytes: K is read 8 bytes a
-// lane, half a warp (4 rows) at a time, V 4 bytes a lane from the 4 rows of the
-// even (then the odd) columns, and either 4 rows must fall on 4 different
-// 32-byte quarters of the 128 banks: rows r with r % 2 and r / 4 different
-// (D = 128: 0 1 4 5 3 2 7 6), or with r % 4 different (D = 64: 0 1 2 3 5 4 7 6).
+// INT4 tiles are read with ldmatrix and need none.
 template <int kKv, int kD>
 __device__ __forceinline__ int tau(int n) {
-    if constexpr (kKv == kKvInt4 && kD == 128)
-        return ((n & 2) << 1) | ((n & 4) >> 1) | ((n ^ (n >> 2)) & 1);
-    else if constexpr (kKv == kKvInt4)
-        return n ^ (n >> 2);
-    else
-        return n ^ ((n & 1) << 2);
+    return kKv == kKvInt4 ? n : n ^ ((n & 1) << 2);
 }
 
 // Units are counted over the chunks that hold a visible token.  With a window,
@@ -777,25 +768,25 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         for (int i = 0; i < 4; ++i)
             v_off[i] = swz<C::kRowBytes, C::kSwizzle>(vr[i], (kD == 128 ? 16 : 8) * g);
     }
-    // INT4: per group, K bytes [8c, 8c+8) of rows tau(g), 8+tau(g); V bytes
-    // [4g, 4g+4) of rows tau(2c), tau(2c+1), 8+.., 8+..
-    uint32_t k4_off[2][C::kGroups], v4_off[4][C::kGroups];
+    // INT4: the row and 16-byte column of this lane's ldmatrix addresses, per
+    // group of 64 dims.  K (matrices: rows 0-7 and 8-15 of the group's first
+    // half, then of its second): a lane gets the 8 dims 8c.. of row g, g + 8,
+    // then the dims 32 + 8c...  V (transposed; token rows 0-7 of both halves,
+    // then 8-15): a lane gets dims 4g.. of tokens 2c and 2c + 1 in one word.
+    uint32_t k4_off[C::kGroups], v4_off[C::kGroups];
     if constexpr (kInt4) {
+        const int r8 = lane & 7, m = lane >> 3;
 #pragma unroll
         for (int gr = 0; gr < C::kGroups; ++gr) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                k4_off[i][gr] = swz<C::kRowBytes, C::kSwizzle>(row0 + 8 * i + tok(g), 32 * gr + 8 * c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v4_off[i][gr] = swz<C::kRowBytes, C::kSwizzle>(
-                    row0 + 8 * (i >> 1) + tok(2 * c + (i & 1)), 32 * gr + 4 * g);
+            k4_off[gr] = swz<C::kRowBytes, C::kSwizzle>(row0 + r8 + 8 * (m & 1), 32 * gr + 16 * (m >> 1));
+            v4_off[gr] = swz<C::kRowBytes, C::kSwizzle>(row0 + r8 + 8 * (m >> 1), 32 * gr + 16 * (m & 1));
         }
     }
 
-    // This warp's query rows of a segment as raw words: FP8 and INT4, per n-block and
-    // 64-dim part the 16 bf16 dims [16c, 16c+16) (8 words); BF16, the two
-    // B-operand words of each k-step.  Heads past the group read as zero.
+    // This warp's query rows of a segment as raw words: FP8, per n-block and
+    // 64-dim part the 16 bf16 dims [16c, 16c+16) (8 words), INT4 the dims
+    // [8c, 8c+8) and [32+8c, 32+8c+8); BF16, the two B-operand words of each
+    // k-step.  Heads past the group read as zero.
     constexpr int kQWords = C::kQWords;
     auto load_q = [&](const Segment& sg, uint32_t (&w)[kQWords]) {
         const int64_t hw0 = static_cast<int64_t>(sg.b) * a.num_q_heads + sg.h * IQ + kvh_w * G;
@@ -807,8 +798,8 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if constexpr (kKv != kKvBf16) {
 #pragma unroll
                 for (int part = 0; part < kD / 64; ++part) {
-                    const uint4* src = reinterpret_cast<const uint4*>(qrow + part * 64 + 16 * c);
-                    const uint4 w0 = src[0], w1 = src[1];
+                    const uint4* src = reinterpret_cast<const uint4*>(qrow + part * 64 + (kInt4 ? 8 : 16) * c);
+                    const uint4 w0 = src[0], w1 = src[kInt4 ? 4 : 1];
                     uint32_t* d = &w[(nb * (kD / 64) + part) * 8];
                     d[0] = valid ? w0.x : 0u; d[1] = valid ? w0.y : 0u;
                     d[2] = valid ? w0.z : 0u; d[3] = valid ? w0.w : 0u;
@@ -899,7 +890,10 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // ---- Q^T as the B operand: column n = head g (+8 per n-block) -----
         uint32_t qb[kNB][kKS][2];
         float qs[kNB][2];   // score scale of S columns 2c and 2c+1
-        float qm[kNB][C::kGroups][2];   // INT4: scaled sum of the group's query dims, same columns
+        // INT4: B operand of the minima's product.  A parameter word (s, m) is an
+        // A operand pair as it is; B is 0 for s, and for m a bf16 part of the
+        // group's scaled query sum: three parts make its 24 bits.
+        uint32_t qy[kNB][2];
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb) {
             float my_scale;
@@ -934,8 +928,9 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const float up = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
                 if constexpr (kInt4) {
                     // k-step 4 part + i takes nibble i of the low and of the high
-                    // half of K words 0 and 1: dims i, i + 4 and 8 + i, 12 + i of
+                    // half of the two K words: dims i, i + 4 and 8 + i, 12 + i of
                     // the thread's 16.  Odd i reads 16 times the code (see below).
+                    uint32_t parts[C::kGroups][3];
 #pragma unroll
                     for (int part = 0; part < C::kGroups; ++part) {
                         const float* w = v + 16 * part;
@@ -945,14 +940,30 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                         sum *= a.qk_scale;
-                        qm[nb][part][0] = __shfl_sync(0xffffffffu, sum, 4 * (2 * c));
-                        qm[nb][part][1] = __shfl_sync(0xffffffffu, sum, 4 * (2 * c + 1));
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            parts[part][k] = static_cast<uint32_t>(f32_to_bf16_bits(sum)) << 16;
+                            sum -= __uint_as_float(parts[part][k]);
+                        }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float u = (i & 1) ? up * 0.0625f : up;
                             qb[nb][4 * part + i][0] = pack_f16x2(w[i] * u, w[i + 4] * u);
                             qb[nb][4 * part + i][1] = pack_f16x2(w[8 + i] * u, w[12 + i] * u);
                         }
+                    }
+                    // k slots: lanes c read the word of group c % 2 (one group: its
+                    // only word); parts 0 and 1 in the first half, 2 in the second
+                    if constexpr (C::kGroups == 2) {
+                        const bool odd = (c & 1) != 0;
+                        const uint32_t p0 = odd ? parts[1][0] : parts[0][0];
+                        const uint32_t p1 = odd ? parts[1][1] : parts[0][1];
+                        const uint32_t p2 = odd ? parts[1][2] : parts[0][2];
+                        qy[nb][0] = c < 2 ? p0 : p1;
+                        qy[nb][1] = c < 2 ? p2 : 0u;
+                    } else {
+                        qy[nb][0] = c == 0 ? parts[0][0] : (c == 1 ? parts[0][1] : (c == 2 ? parts[0][2] : 0u));
+                        qy[nb][1] = 0u;
                     }
                     // (the codes read as code * 2^-24)
                     my_scale = a.qk_scale * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23) *
@@ -995,13 +1006,17 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
         // INT4: O holds sum_t w_t s_t code_t / vref, with vref (a power of two,
         // common to the warp) keeping the f16 weights w_t s_t / vref in range, and
-        // vb the part of the groups' minima, sum_t w_t m_t, in binary32.
-        float vref = 0.f, vinv = 0.f, vbias[kNB][C::kGroups][2];
+        // vbias the part of the groups' minima, sum_t w_t m_t, in binary32.  Scores
+        // are held relative to m (0 before the first visible token, when `bound`
+        // lets every score raise it).
+        float vref = 0.f, vinv = 0.f, vbias[kNB][C::kGroups][2], bound = kNegInf;
         if constexpr (kInt4) {
 #pragma unroll
-            for (int nb = 0; nb < kNB; ++nb)
+            for (int nb = 0; nb < kNB; ++nb) {
+                m[nb][0] = m[nb][1] = 0.f;
 #pragma unroll
                 for (int gr = 0; gr < C::kGroups; ++gr) vbias[nb][gr][0] = vbias[nb][gr][1] = 0.f;
+            }
         }
         int poisoned = 0;
 
@@ -1022,13 +1037,209 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             };
             const uint32_t kb_head = smem_addr(smem + stage * C::kStageBytes) + kvh_w * C::kHeadTileBytes;
             const uint32_t vb_head = kb_head + C::kTileBytes;
+            if constexpr (kInt4) {
+                // kH tiles of 16 tokens (rows row0 + 16 t ..) and 8 kNB heads.
+                // (1) sum of q . code per group: a code in bits 0-3 (4-7) of an f16
+                // whose other bits are zero reads as the subnormal code * 2^-24
+                // (* 2^-20), exactly, so one AND makes an operand pair.
+                float acc[kH][kNB][C::kGroups][4];
+#pragma unroll
+                for (int t = 0; t < kH; ++t) {
+#pragma unroll
+                    for (int gr = 0; gr < C::kGroups; ++gr) {
+                        uint32_t x[4];
+                        ldsm_x4(kb_head + k4_off[gr] + t * 16 * C::kRowBytes, x[0], x[1], x[2], x[3]);
+#pragma unroll
+                        for (int nb = 0; nb < kNB; ++nb)
+                            acc[t][nb][gr][0] = acc[t][nb][gr][1] = acc[t][nb][gr][2] =
+                                acc[t][nb][gr][3] = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t msk = (i & 1) ? 0x00F000F0u : 0x000F000Fu;
+                            if (i == 2) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) x[k] >>= 8;
+                            }
+#pragma unroll
+                            for (int nb = 0; nb < kNB; ++nb)
+                                mma_f16(acc[t][nb][gr], x[0] & msk, x[1] & msk, x[2] & msk, x[3] & msk,
+                                        qb[nb][4 * gr + i][0], qb[nb][4 * gr + i][1]);
+                        }
+                    }
+                }
+                // (2) scores less m, in log2 units: p = qs sum_gr scale (q . code)
+                // + (sum_gr minimum sum(q) - m), the bracket one bf16 MMA on the raw
+                // parameter words.  p[t][nb][0..1]: token row g, heads 2c, 2c+1;
+                // [2..3]: row g + 8.
+                float p[kH][kNB][4];
+                float vs[kH][2][C::kGroups], vm[kH][2][C::kGroups];   // V's of rows g, g + 8
+                float vtop = 0.f, ptop = kNegInf;
+                const uint32_t par = smem_addr(smem + stage * C::kStageBytes) + 2 * C::kTileBytes +
+                                     (kvh_w * kChunkTokens + row0 + g) * kPR;
+#pragma unroll
+                for (int t = 0; t < kH; ++t) {
+                    float ks[2][C::kGroups];
+                    uint32_t kw[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t kp = par + (16 * t + 8 * i) * kPR, vp = kp + C::kParTileBytes;
+                        if constexpr (C::kGroups == 2) {
+                            const uint2 x = lds64(kp), y = lds64(vp);
+                            kw[i] = lds32(kp + 4 * (c & 1));
+                            ks[i][0] = bf16_bits_to_f32(x.x);
+                            ks[i][1] = bf16_bits_to_f32(x.y);
+                            bf16x2_to_f32x2(y.x, vs[t][i][0], vm[t][i][0]);
+                            bf16x2_to_f32x2(y.y, vs[t][i][1], vm[t][i][1]);
+                        } else {
+                            kw[i] = lds32(kp);
+                            ks[i][0] = bf16_bits_to_f32(kw[i]);
+                            bf16x2_to_f32x2(lds32(vp), vs[t][i][0], vm[t][i][0]);
+                        }
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < kNB; ++nb) {
+                        float y[4] = {-m[nb][0], -m[nb][1], -m[nb][0], -m[nb][1]};
+                        mma_bf16(y, kw[0], kw[1], kw[0], kw[1], qy[nb][0], qy[nb][1]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float x = ks[e >> 1][0] * acc[t][nb][0][e];
+                            if constexpr (C::kGroups == 2)
+                                x = fmaf(ks[e >> 1][1], acc[t][nb][1][e], x);
+                            p[t][nb][e] = fmaf(x, qs[nb][e & 1], y[e]);
+                        }
+                    }
+                }
+                if (tail) {
+#pragma unroll
+                    for (int t = 0; t < kH; ++t)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (masked(row0 + 16 * t + 8 * i + g)) {
+#pragma unroll
+                                for (int nb = 0; nb < kNB; ++nb)
+                                    p[t][nb][2 * i] = p[t][nb][2 * i + 1] = kNegInf;
+#pragma unroll
+                                for (int gr = 0; gr < C::kGroups; ++gr) vs[t][i][gr] = vm[t][i][gr] = 0.f;
+                            }
+                }
+                // (3) lazy rescaling, as below, and of vref with V's scales
+#pragma unroll
+                for (int t = 0; t < kH; ++t) {
+#pragma unroll
+                    for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) ptop = fmaxf(ptop, p[t][nb][e]);
+#pragma unroll
+                    for (int gr = 0; gr < C::kGroups; ++gr)
+                        vtop = fmaxf(vtop, fmaxf(fabsf(vs[t][0][gr]), fabsf(vs[t][1][gr])));
+                }
+                if (__any_sync(0xffffffffu, ptop > bound || vtop > 64.f * vref)) {
+                    // the largest scale so far as a power of two, within [2^-100, 2^126]
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1)
+                        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
+                    const uint32_t ve = min(max(__float_as_uint(vtop) >> 23, 27u), 253u);
+                    const float now = fmaxf(vref, __uint_as_float(ve << 23));
+                    vinv = __uint_as_float((254u - (__float_as_uint(now) >> 23)) << 23);
+                    const float vfix = vref * vinv;
+                    vref = now;
+                    bool any = false;
+#pragma unroll
+                    for (int nb = 0; nb < kNB; ++nb) {
+                        float alpha[2];
+#pragma unroll
+                        for (int col = 0; col < 2; ++col) {
+                            float up = kNegInf;   // the largest score less m
+#pragma unroll
+                            for (int t = 0; t < kH; ++t)
+                                up = fmaxf(up, fmaxf(p[t][nb][col], p[t][nb][col + 2]));
+                            up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 4));
+                            up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
+                            up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16));
+                            any |= up != kNegInf;
+                            // m rises; the first visible scores set it either way
+                            up = (up == kNegInf) ? 0.f : (bound == kNegInf ? up : fmaxf(up, 0.f));
+                            alpha[col] = bound == kNegInf ? 0.f : exp2f(-up);
+                            m[nb][col] += up;
+                            l[nb][col] *= alpha[col];
+#pragma unroll
+                            for (int gr = 0; gr < C::kGroups; ++gr) vbias[nb][gr][col] *= alpha[col];
+                            alpha[col] *= vfix;
+#pragma unroll
+                            for (int t = 0; t < kH; ++t) {
+                                p[t][nb][col] -= up;
+                                p[t][nb][col + 2] -= up;
+                            }
+                        }
+#pragma unroll
+                        for (int mb = 0; mb < kMB; ++mb) {
+                            o[nb][mb][0] *= alpha[0];
+                            o[nb][mb][1] *= alpha[1];
+                            o[nb][mb][2] *= alpha[0];
+                            o[nb][mb][3] *= alpha[1];
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, any)) bound = kRescaleThreshold;
+                }
+                // (4) weights, and O^T[16 dims][8 heads] += V^T P^T.  The f16 weight of
+                // a group is w scale / vref: w is at most 2^8 and scale / vref below
+                // 64, so it stays below 2^14.  After the transposing load the low
+                // (high) halves of a word are two tokens' dims 4g .. 4g + 3: m-block
+                // 2 gr' + i takes nibble 2i (accumulator rows g, code * 2^-24) and
+                // 2i + 1 (rows g + 8, code * 2^-20).  Masked tokens have zero weights,
+                // and every code is a finite number.
+#pragma unroll
+                for (int t = 0; t < kH; ++t) {
+                    uint32_t pb[kNB][C::kGroups][2];
+#pragma unroll
+                    for (int nb = 0; nb < kNB; ++nb) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            p[t][nb][e] = ex2_approx(p[t][nb][e]);
+                            l[nb][e & 1] += p[t][nb][e];
+                        }
+#pragma unroll
+                        for (int gr = 0; gr < C::kGroups; ++gr) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float w = vs[t][i][gr] * vinv;
+                                pb[nb][gr][i] = movmatrix_trans(
+                                    pack_f16x2(p[t][nb][2 * i] * w, p[t][nb][2 * i + 1] * w));
+#pragma unroll
+                                for (int col = 0; col < 2; ++col)
+                                    vbias[nb][gr][col] =
+                                        fmaf(p[t][nb][2 * i + col], vm[t][i][gr], vbias[nb][gr][col]);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int gr = 0; gr < C::kGroups; ++gr) {
+                        // x[0], x[1]: tokens 2c, 2c+1, dims 4g.. of the halves; x[2], x[3]:
+                        // tokens 8 + 2c, 8 + 2c + 1
+                        uint32_t x[4];
+                        ldsm_x4_trans(vb_head + v4_off[gr] + t * 16 * C::kRowBytes, x[0], x[1], x[2], x[3]);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t lo = k ? x[half] >> 8 : x[half];
+                                const uint32_t hi = k ? x[2 + half] >> 8 : x[2 + half];
+#pragma unroll
+                                for (int nb = 0; nb < kNB; ++nb)
+                                    mma_f16(o[nb][4 * gr + 2 * half + k], lo & 0x000F000Fu,
+                                            lo & 0x00F000F0u, hi & 0x000F000Fu, hi & 0x00F000F0u,
+                                            pb[nb][gr][0], pb[nb][gr][1]);
+                            }
+                    }
+                }
+            } else {
 #pragma unroll
             for (int t = 0; t < kH; ++t) {
             const int rb = row0 + 16 * t;
             // FP8 offsets are relative to the warp's first tile; 16 rows on, the
             // swizzle pattern repeats, so the next tile is a plain offset
-            const uint32_t kb = kb_head + (kKv != kKvBf16 ? t * 16 * C::kRowBytes : 0);
-            const uint32_t vb = vb_head + (kKv != kKvBf16 ? t * 16 * C::kRowBytes : 0);
+            const uint32_t kb = kb_head + (kFp8 ? t * 16 * C::kRowBytes : 0);
+            const uint32_t vb = vb_head + (kFp8 ? t * 16 * C::kRowBytes : 0);
 
             // ---- S[16 tokens][8 heads] = K Q^T, two accumulator chains ------
             float acc[kNB][2][4];
@@ -1054,26 +1265,6 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     for (int nb = 0; nb < kNB; ++nb)
                         mma_f16(acc[nb][j & 1], a0, a1, a2, a3, qb[nb][j][0], qb[nb][j][1]);
                 }
-            } else if constexpr (kInt4) {
-                // A 4-bit code in bits 0-3 (4-7) of an f16 whose other bits are
-                // zero reads as the subnormal code * 2^-24 (* 2^-20), exactly: one
-                // AND turns two codes of a word into an operand pair.
-#pragma unroll
-                for (int gr = 0; gr < C::kGroups; ++gr) {
-                    uint2 x = lds64(kb + k4_off[0][gr]);
-                    uint2 y = lds64(kb + k4_off[1][gr]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t msk = (i & 1) ? 0x00F000F0u : 0x000F000Fu;
-                        if (i == 2) {
-                            x.x >>= 8; x.y >>= 8; y.x >>= 8; y.y >>= 8;
-                        }
-#pragma unroll
-                        for (int nb = 0; nb < kNB; ++nb)
-                            mma_f16(acc[nb][C::kGroups == 2 ? gr : (i & 1)], x.x & msk, y.x & msk,
-                                    x.y & msk, y.y & msk, qb[nb][4 * gr + i][0], qb[nb][4 * gr + i][1]);
-                    }
-                }
             } else {
                 const int q8 = lane >> 3;
                 const int row = rb + 8 * (q8 & 1) + (lane & 7);
@@ -1093,68 +1284,18 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // ---- online softmax over the 16 tokens, per head (log2 units) ----
             // p[nb][0..1]: token row g, heads 2c, 2c+1; p[nb][2..3]: row g + 8
             float p[kNB][4];
-            // INT4: V's (scale, minimum) of this thread's two tokens, per group
-            float vs[2][C::kGroups], vm[2][C::kGroups];
-            float vtop = 0.f;
-            if constexpr (kInt4) {
-                // s_t = qk_scale (sum_gr scale_t,gr (q . code)_gr + minimum_t,gr sum(q)_gr)
-                const uint32_t kp = kb_head + 2 * C::kTileBytes - kvh_w * C::kHeadTileBytes +
-                                    (kvh_w * kChunkTokens + rb + tok(g)) * kPR;
-                const uint32_t vp = kp + C::kParTileBytes;
-                uint32_t kw[2][2], vw[2][2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if constexpr (C::kGroups == 2) {
-                        const uint2 x = lds64(kp + 8 * i * kPR), y = lds64(vp + 8 * i * kPR);
-                        kw[i][0] = x.x; kw[i][1] = x.y; vw[i][0] = y.x; vw[i][1] = y.y;
-                    } else {
-                        kw[i][0] = lds32(kp + 8 * i * kPR); vw[i][0] = lds32(vp + 8 * i * kPR);
-                    }
-                }
+            for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float ks[C::kGroups], km[C::kGroups];
-#pragma unroll
-                    for (int gr = 0; gr < C::kGroups; ++gr) {
-                        bf16x2_to_f32x2(kw[i][gr], ks[gr], km[gr]);
-                        bf16x2_to_f32x2(vw[i][gr], vs[i][gr], vm[i][gr]);
-                    }
-#pragma unroll
-                    for (int nb = 0; nb < kNB; ++nb)
-#pragma unroll
-                        for (int col = 0; col < 2; ++col) {
-                            float x = 0.f, y = 0.f;
-                            if constexpr (C::kGroups == 2) {
-                                x = ks[0] * acc[nb][0][2 * i + col] + ks[1] * acc[nb][1][2 * i + col];
-                                y = km[0] * qm[nb][0][col] + km[1] * qm[nb][1][col];
-                            } else {
-                                x = ks[0] * (acc[nb][0][2 * i + col] + acc[nb][1][2 * i + col]);
-                                y = km[0] * qm[nb][0][col];
-                            }
-                            p[nb][2 * i + col] = fmaf(x, qs[nb][col], y);
-                        }
-                }
-            } else {
-#pragma unroll
-                for (int nb = 0; nb < kNB; ++nb)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        p[nb][i] = (acc[nb][0][i] + acc[nb][1][i]) * qs[nb][i & 1];
-            }
+                for (int i = 0; i < 4; ++i)
+                    p[nb][i] = (acc[nb][0][i] + acc[nb][1][i]) * qs[nb][i & 1];
             if (tail) {
-                const int t_lo = kKv != kKvBf16 ? rb + tok(g) : rb + g;
+                const int t_lo = kFp8 ? rb + tok(g) : rb + g;
                 const int t_hi = t_lo + 8;
 #pragma unroll
                 for (int nb = 0; nb < kNB; ++nb) {
                     if (masked(t_lo)) p[nb][0] = p[nb][1] = kNegInf;
                     if (masked(t_hi)) p[nb][2] = p[nb][3] = kNegInf;
-                }
-                if constexpr (kInt4) {
-#pragma unroll
-                    for (int gr = 0; gr < C::kGroups; ++gr) {
-                        if (masked(t_lo)) vs[0][gr] = vm[0][gr] = 0.f;
-                        if (masked(t_hi)) vs[1][gr] = vm[1][gr] = 0.f;
-                    }
                 }
             }
             // Lazy rescaling: the running max m (uniform over the warp, per head)
@@ -1166,25 +1307,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
                 for (int col = 0; col < 2; ++col)
                     need |= fmaxf(p[nb][col], p[nb][col + 2]) > m[nb][col] + kRescaleThreshold;
-            if constexpr (kInt4) {
-#pragma unroll
-                for (int gr = 0; gr < C::kGroups; ++gr)
-                    vtop = fmaxf(vtop, fmaxf(fabsf(vs[0][gr]), fabsf(vs[1][gr])));
-                need |= vtop > 64.f * vref;
-            }
             if (__any_sync(0xffffffffu, need)) {
-                float vfix = 1.f;
-                if constexpr (kInt4) {
-                    // the largest scale so far as a power of two, within [2^-100, 2^126]
-#pragma unroll
-                    for (int off = 4; off < 32; off <<= 1)
-                        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
-                    const uint32_t e = min(max(__float_as_uint(vtop) >> 23, 27u), 253u);
-                    const float now = fmaxf(vref, __uint_as_float(e << 23));
-                    vinv = __uint_as_float((254u - (__float_as_uint(now) >> 23)) << 23);
-                    vfix = vref * vinv;
-                    vref = now;
-                }
 #pragma unroll
                 for (int nb = 0; nb < kNB; ++nb) {
                     float alpha[2];
@@ -1200,15 +1323,6 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         l[nb][col] *= alpha[col];
                         lr[nb][col] *= alpha[col];
                     }
-                    if constexpr (kInt4) {
-#pragma unroll
-                        for (int gr = 0; gr < C::kGroups; ++gr) {
-                            vbias[nb][gr][0] *= alpha[0];
-                            vbias[nb][gr][1] *= alpha[1];
-                        }
-                        alpha[0] *= vfix;
-                        alpha[1] *= vfix;
-                    }
 #pragma unroll
                     for (int mb = 0; mb < kMB; ++mb) {
                         o[nb][mb][0] *= alpha[0];
@@ -1220,7 +1334,6 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
             // P^T as the PV B operand: k = token row, n = head g
             uint32_t pb[kNB][2];
-            uint32_t pb4[kNB][C::kGroups][2];   // INT4: weights times each group's scale
 #pragma unroll
             for (int nb = 0; nb < kNB; ++nb) {
 #pragma unroll
@@ -1230,24 +1343,6 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 l[nb][0] += p[nb][0] + p[nb][2];
                 l[nb][1] += p[nb][1] + p[nb][3];
-                if constexpr (kInt4) {
-                    // f16 weights (2^-11 of each at most): a weight is at most 2^8 and
-                    // scale / vref below 64, so the product stays below 2^14
-#pragma unroll
-                    for (int gr = 0; gr < C::kGroups; ++gr) {
-                        const float w0 = vs[0][gr] * vinv, w1 = vs[1][gr] * vinv;
-                        pb4[nb][gr][0] =
-                            movmatrix_trans(pack_f16x2(p[nb][0] * w0, p[nb][1] * w0));
-                        pb4[nb][gr][1] =
-                            movmatrix_trans(pack_f16x2(p[nb][2] * w1, p[nb][3] * w1));
-#pragma unroll
-                        for (int col = 0; col < 2; ++col)
-                            vbias[nb][gr][col] = fmaf(p[nb][col], vm[0][gr],
-                                                      fmaf(p[nb][col + 2], vm[1][gr],
-                                                           vbias[nb][gr][col]));
-                    }
-                    continue;
-                }
                 uint32_t h01, h23;
                 float r0, r1, r2, r3;
                 if constexpr (kFp8) {
@@ -1307,32 +1402,6 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     for (int nb = 0; nb < kNB; ++nb)
                         mma_f16(o[nb][2 * q + 1], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
                 }
-            } else if constexpr (kInt4) {
-                // word [4g, 4g+4) of a group holds its dims 8g..8g+7: m-block
-                // 4 gr + i takes dims 2i (accumulator rows g, code * 2^-24) and
-                // 2i + 1 (rows g + 8, code * 2^-20).  Masked tokens have zero
-                // weights, and every code is a finite number.
-#pragma unroll
-                for (int gr = 0; gr < C::kGroups; ++gr) {
-                    uint32_t x[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) x[r] = lds32(vb + v4_off[r][gr]);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t sel = half ? 0x7632u : 0x5410u;
-                        uint32_t t01 = prmt(x[0], x[1], sel), t23 = prmt(x[2], x[3], sel);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                            for (int nb = 0; nb < kNB; ++nb)
-                                mma_f16(o[nb][4 * gr + 2 * half + k], t01 & 0x000F000Fu,
-                                        t01 & 0x00F000F0u, t23 & 0x000F000Fu, t23 & 0x00F000F0u,
-                                        pb4[nb][gr][0], pb4[nb][gr][1]);
-                            t01 >>= 8;
-                            t23 >>= 8;
-                        }
-                    }
-                }
             } else {
                 const int q8 = lane >> 3;
                 const int row = rb + 8 * (q8 >> 1) + (lane & 7);
@@ -1358,6 +1427,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
             }
             }   // tiles
+            }
             __syncwarp();
             if (lane == 0 && !(C::kRedInStage && ch + 1 == s.c1)) mbar_arrive(&empty_bar[stage]);
         }
@@ -1365,6 +1435,12 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // epilogue
         int next_aborted = 0;
         if constexpr (C::kEarlyQ) next_aborted = have_next ? load_q(sn, qw) : 0;
+        if constexpr (kInt4) {
+            if (bound == kNegInf) {   // no visible token: a partial of weight zero
+#pragma unroll
+                for (int nb = 0; nb < kNB; ++nb) m[nb][0] = m[nb][1] = kNegInf;
+            }
+        }
         const bool whole = whole_of();
         const int64_t head0 = head0_of();
 
@@ -1432,13 +1508,14 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                             o[nb][2 * k + 1][col], o[nb][2 * k + 1][col + 2]);
                         }
                     } else if constexpr (kInt4) {
+                        // dims 32 half + 4g .. of a group: m-blocks 2 half, 2 half + 1
 #pragma unroll
                         for (int gr = 0; gr < C::kGroups; ++gr)
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const uint32_t u = 16 * gr + 2 * g + k;
-                                const float* x = o[nb][4 * gr + 2 * k];
-                                const float* y = o[nb][4 * gr + 2 * k + 1];
+                            for (int half = 0; half < 2; ++half) {
+                                const uint32_t u = 16 * gr + 8 * half + g;
+                                const float* x = o[nb][4 * gr + 2 * half];
+                                const float* y = o[nb][4 * gr + 2 * half + 1];
                                 const float add = vbias[nb][gr][col];
                                 *reinterpret_cast<float4*>(row + 4 * (u ^ sw)) =
                                     make_float4(fmaf(x[col] * 0x1p24f, vref, add),
