@@ -316,6 +316,25 @@ pkv_status plan_attention(int kv, int32_t batch, int32_t num_kv_heads, int32_t g
         if (cluster == 0 && num_ctas < 0)
             return fail(PKV_ERR_UNSUPPORTED, "clusters of %d CTAs do not fit on this device",
                         -num_ctas);
+        // INT4: split-K uses every resident CTA and costs a merge launch, about the
+        // time of two or three chunks of a CTA.  It is taken where the longest
+        // requests that the page table allows leave a CTA that many fewer (measured,
+        // cluster / split-K, 8 KV heads of 128 dims: 1 x 32,768 tokens 42 / 27 us, 4 x
+        // 8,192 28 / 28, 8 x 2,048 20 / 23, 8 x 32,768 132 / 81, 16 x 8,192 48 / 50,
+        // 64 x 8,192 147 / 135).
+        if (num_ctas == 0 && kv == PKV_KV_INT4 && cluster > 0) {
+            const int64_t chunks = (max_visible(max_pages, page_size, window, sinks) +
+                                    pkv::kChunkTokens - 1) / pkv::kChunkTokens;
+            const int wide = plan->ws_kv_per_item;
+            const double in_cluster = static_cast<double>((items + nclusters - 1) / nclusters) *
+                                      chunks / cluster * kv_per_item / wide;
+            const double in_split =
+                static_cast<double>(batch) * (num_kv_heads / wide) * chunks / grid;
+            if (in_cluster - in_split > 2.5) {
+                cluster = nclusters = 0;
+                kv_per_item = wide;
+            }
+        }
     }
     plan->kv_per_item = kv_per_item;
     plan->cluster = cluster;
@@ -386,11 +405,11 @@ pkv_status attn_impl(const KvPools& pools, const uint16_t* q, const int32_t* pag
                     wl.total);
 
     // rows of one TMA box: a 64-token chunk of a page (a whole page when
-    // smaller); with two KV heads per item and 64-token pages, both heads' rows
-    // of the page at once (they are adjacent in the pool)
-    const int box_rows = (kv_per_item == 2 && page_size == pkv::kChunkTokens)
-                             ? 2 * pkv::kChunkTokens
-                             : (page_size < pkv::kChunkTokens ? page_size : pkv::kChunkTokens);
+    // smaller); with two KV heads per item and 64-token pages (INT4: up to 64),
+    // both heads' rows of the page at once (they are adjacent in the pool)
+    const bool joint = kv_per_item == 2 && (page_size == pkv::kChunkTokens ||
+                                            (int4 && page_size < pkv::kChunkTokens));
+    const int box_rows = std::min<int>(page_size, pkv::kChunkTokens) * (joint ? 2 : 1);
     const int64_t rows = static_cast<int64_t>(num_pages) * num_kv_heads * page_size;
     CUtensorMap tk, tv;
     st = encode_pool_map(&tk, k_cache, kv, head_dim, rows, box_rows);
@@ -424,6 +443,8 @@ pkv_status attn_impl(const KvPools& pools, const uint16_t* q, const int32_t* pag
     a.num_clusters = nclusters;
     a.qk_scale = sm_scale * (fp8 ? k_scale : 1.f) * 1.4426950408889634f;
     a.v_scale = fp8 ? v_scale : 1.f;
+    a.k_codes = int4 ? static_cast<const uint8_t*>(k_cache) : nullptr;
+    a.v_codes = int4 ? static_cast<const uint8_t*>(v_cache) : nullptr;
     a.k_params = reinterpret_cast<const uint8_t*>(pools.k_params);
     a.v_params = reinterpret_cast<const uint8_t*>(pools.v_params);
     a.window = window;

@@ -67,6 +67,13 @@ struct AttnCfg {
     static constexpr int kGroups = kInt4 ? kD / kInt4Group : 1;
     static constexpr int kParRowBytes = kInt4 ? 4 * kGroups : 0;
     static constexpr int kParTileBytes = kH * kChunkTokens * kParRowBytes;
+    // INT4 pages of at most this many tokens are copied 16 bytes a lane by the
+    // whole producer warp; larger ones as TMA boxes.  A box costs its one issuing
+    // lane the same whatever its size, so it pays from 8 KB of codes on.  Measured
+    // (444 CTAs, TMA / copies): D = 128, 64 x 8,192 tokens, pages of 64: 135 / 149 us,
+    // of 32: 179 / 148, of 16: 242 / 149; D = 64, 96 ragged requests, pages of 64:
+    // 79 / 73, of 32: 110 / 73, of 16: 163 / 77.
+    static constexpr int kDirectPage = kInt4 ? (kD == 128 ? 32 : 64) : 0;
     static constexpr int kStageBytes = (2 * (kTileBytes + kParTileBytes) + 1023) / 1024 * 1024;
     // Pipeline depth and resident CTAs per SM, chosen by measurement on B200:
     // resident warps matter more than depth (each CTA keeps up to kStages
@@ -429,7 +436,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ AttnArgs a) {
     using C = AttnCfg<kKv, kD, kGP, kH>;
     constexpr bool kFp8 = C::kFp8, kInt4 = C::kInt4;
-    constexpr int kPR = C::kParRowBytes;   // INT4: bytes of a token's parameters
+    constexpr int kPR = C::kParRowBytes;   // INT4: bytes of a token's parameters (else 0)
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -470,7 +477,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
     if (blockIdx.x == 0 && tid == 0 && a.chunk_begin == nullptr) *a.ws_status = 0u;
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full_bar[s], 1);
+            mbar_init(&full_bar[s], kInt4 && a.page_size <= C::kDirectPage ? 33 : 1);
             mbar_init(&empty_bar[s], kConsumerWarps);
         }
         *cta_failed = 0;
@@ -567,18 +574,22 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
 
     const int P = a.page_size;
     const int box_rows = a.box_rows;
-    // With two KV heads per item and 64-token pages, the item's K (or V) rows
-    // of a page are one contiguous 128-row box; otherwise one box per KV head
-    // and page (per 64 rows for 128-token pages).
-    const bool joint = (kH == 2) && (box_rows == 2 * kChunkTokens);
-    const int boxes = joint ? 1 : kChunkTokens / box_rows;
+    // With two KV heads per item and 64-token pages (INT4: up to 64), the
+    // item's K (or V) rows of a page are one contiguous box; otherwise one box
+    // per KV head and page (per 64 rows for 128-token pages).
+    const bool joint = (kH == 2) && (kInt4 ? P <= kChunkTokens : box_rows == 2 * kChunkTokens);
+    const int box_toks = joint ? box_rows / 2 : box_rows;
+    const int boxes = kChunkTokens / box_toks;
+    // INT4 with small pages: the producer's lanes copy 16 bytes each instead of
+    // one of them issuing a TMA box per page.
+    const bool direct = kInt4 && P <= C::kDirectPage;
 
-    // With a window: whether the box_rows tokens from tok0 on are all hidden
+    // With a window: whether the box_toks tokens from tok0 on are all hidden
     // (their page-table entry is then not used).
     auto hidden_box = [&](int len, int tok0) {
         if constexpr (kWin) {
             const int lo = len - a.window;
-            return tok0 >= a.sinks && tok0 + (joint ? kChunkTokens : box_rows) <= lo;
+            return tok0 >= a.sinks && tok0 + box_toks <= lo;
         } else {
             return false;
         }
@@ -601,7 +612,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 for (int ch = s.c0; ch < s.c1 && count < S; ++ch, ++count) {
                     const int rc = s.real(ch);
                     for (int i = 0; i < boxes; ++i) {
-                        const int tok0 = rc * kChunkTokens + i * box_rows;
+                        const int tok0 = rc * kChunkTokens + i * box_toks;
                         const int j = tok0 / P;
                         if (j >= npages) break;
                         if (hidden_box(s.L, tok0)) continue;
@@ -638,6 +649,78 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
             return (a.abort != nullptr) ? static_cast<int>(a.abort[sg.b]) : 0;
         };
+        // The loads of a segment, 16 bytes a lane.  The boxes of a chunk are
+        // consecutive page-table entries (lane bx < boxes holds box bx) and
+        // consecutive rows of the tile, so a warp's 512 bytes lie in one box, and
+        // the swizzle, which takes address bits 7 and 8, is the lane's alone.
+        auto copy_segment = [&](const Segment& sg, PageWindow& w, int npages, uint32_t& iter) {
+            constexpr int kSteps = C::kTileBytes / 512;
+            constexpr int kParPieces = C::kParTileBytes / 16;
+            const uint32_t lane_off = swz<C::kRowBytes, C::kSwizzle>(0, lane * 16);
+            const int pshift = 31 - __clz(P);
+            const int steps_shift = 31 - __clz(box_rows * C::kRowBytes / 512);   // steps of a box
+            const int rows_shift = 31 - __clz(box_rows);
+            const int32_t* row = w.row;
+            int ahead_base = -1;      // the entries after the window's, loaded ahead
+            int32_t ahead = -1;
+            for (int ch = sg.c0; ch < sg.c1; ++ch, ++iter) {
+                const int stage = iter % S;
+                const int tok0 = sg.real(ch) * kChunkTokens;
+                const int j0 = tok0 >> pshift;
+                if (j0 - w.base >= 32 || j0 < w.base) {
+                    w.mine = j0 == ahead_base ? ahead : (j0 + lane < npages ? row[j0 + lane] : -1);
+                    w.base = j0;
+                }
+                if (ahead_base != w.base + 32) {
+                    ahead_base = w.base + 32;
+                    ahead = ahead_base + lane < npages ? row[ahead_base + lane] : -1;
+                }
+                const int bx = lane & (boxes - 1);
+                const int32_t pid = __shfl_sync(0xffffffffu, w.mine, j0 - w.base + bx);
+                const bool wanted = j0 + bx < npages && !hidden_box(sg.L, tok0 + bx * box_toks);
+                const bool known = pid >= 0 && pid < a.num_pages;
+                const uint32_t use = __ballot_sync(0xffffffffu, wanted && known);
+                const bool bad = __any_sync(0xffffffffu, wanted && !known);
+                const int32_t y = (pid * Hkv + sg.h * kH) << pshift;   // first pool row
+                if (iter >= static_cast<uint32_t>(S)) {
+                    if (lane == 0)
+                        wait_or_give_up(&empty_bar[stage], ((iter / S) + 1) & 1, cta_failed, a.ws_status);
+                    __syncwarp();
+                }
+                const uint32_t kdst = smem_addr(smem + stage * C::kStageBytes);
+                if (lane == 0) {
+                    stage_bad[stage] = bad;
+                    mbar_arrive(&full_bar[stage]);
+                }
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st) {
+                    const int b = st >> steps_shift;
+                    const int64_t src = static_cast<int64_t>(__shfl_sync(0xffffffffu, y, b)) * C::kRowBytes +
+                                        (st - (b << steps_shift)) * 512 + lane * 16;
+                    if ((use >> b) & 1) {
+                        const uint32_t dst = kdst + st * 512 + lane_off;
+                        cp_async16(dst, a.k_codes + src);
+                        cp_async16(dst + C::kTileBytes, a.v_codes + src);
+                    }
+                }
+#pragma unroll
+                for (int q0 = 0; q0 < kParPieces; q0 += 32) {
+                    const int q = q0 + lane;
+                    const int r = q * 16 / (kInt4 ? kPR : 1);
+                    const int b = (r >> rows_shift) & (boxes - 1);
+                    const int64_t src = (static_cast<int64_t>(__shfl_sync(0xffffffffu, y, b)) +
+                                         (r & (box_rows - 1))) * kPR;
+                    if (q < kParPieces && ((use >> b) & 1)) {
+                        const uint32_t dst = kdst + 2 * C::kTileBytes + q * 16;
+                        cp_async16(dst, a.k_params + src);
+                        cp_async16(dst + C::kParTileBytes, a.v_params + src);
+                    }
+                }
+                // (a full stage: lane 0's arrival above, which covers the flag, and one
+                // per lane once that lane's copies have landed)
+                cp_async_arrive(&full_bar[stage]);
+            }
+        };
         uint32_t it = 0;
         Segment s;
         bool have = walk.next(s);
@@ -663,7 +746,10 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (lane * 64 < kH * a.group * kD) prefetch_l2(a.q + q0 + lane * 64);
             }
             const int npages = (s.L + P - 1) / P;
-            for (int ch = s.c0; ch < s.c1; ++ch, ++it) {
+            if constexpr (kInt4) {
+                if (direct) copy_segment(s, win, npages, it);
+            }
+            for (int ch = s.c0; ch < s.c1 && !direct; ++ch, ++it) {
                 const int stage = it % S;
                 if (it >= static_cast<uint32_t>(S)) {
                     if (lane == 0) wait_or_give_up(&empty_bar[stage], ((it / S) + 1) & 1, cta_failed, a.ws_status);
@@ -679,7 +765,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 for (int i = 0; i < 4; ++i) {
                     pids[i] = -1;
                     if (i < boxes) {
-                        const int tok0 = rc * kChunkTokens + i * box_rows;
+                        const int tok0 = rc * kChunkTokens + i * box_toks;
                         const int j = tok0 / P;
                         if (j < npages && !hidden_box(s.L, tok0)) {
                             pids[i] = win.get(j, npages, lane);
@@ -699,7 +785,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (pids[i] < 0) continue;
-                        const int tok0 = rc * kChunkTokens + i * box_rows;
+                        const int tok0 = rc * kChunkTokens + i * box_toks;
                         for (int kv = 0; kv < (joint ? 1 : kH); ++kv) {
                             const int32_t y = (pids[i] * Hkv + s.h * kH + kv) * P + (tok0 % P);
                             for (int st = 0; st < C::kSubTiles; ++st) {
@@ -751,6 +837,16 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
     constexpr int kMB = kD / 16;      // m-blocks of the head dimension (PV)
     constexpr int kKS = kD / 16;      // k-steps of the QK contraction
 
+    // INT4: the first row, in a K or V tile of the item, of the warp's 16-token
+    // tile t (rows run token by token inside a page, then over the item's KV heads)
+    auto tile_row = [&](int t) {
+        const int rb = row0 + 16 * t;
+        if constexpr (kH == 1) return rb;
+        return (rb / box_toks * 2 + kvh_w) * box_toks + rb % box_toks;
+    };
+    uint32_t trow[kH];
+#pragma unroll
+    for (int t = 0; t < kH; ++t) trow[t] = kInt4 ? (joint ? tile_row(t) : kvh_w * kChunkTokens + row0 + 16 * t) : 0;
     // Fixed shared-memory offsets of this thread's K and V reads.
     uint32_t k_off[2][kD / 64];       // FP8: rows tau(g), 8+tau(g); chunks c, 4+c
     uint32_t v_off[4];                // FP8: rows tau(2c), tau(2c+1), 8+.., 8+..; chunk g
@@ -768,8 +864,8 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         for (int i = 0; i < 4; ++i)
             v_off[i] = swz<C::kRowBytes, C::kSwizzle>(vr[i], (kD == 128 ? 16 : 8) * g);
     }
-    // INT4: the row and 16-byte column of this lane's ldmatrix addresses, per
-    // group of 64 dims.  K (matrices: rows 0-7 and 8-15 of the group's first
+    // INT4: the row in a 16-row tile and the 16-byte column of this lane's
+    // ldmatrix addresses, per group of 64 dims (16 rows on, the swizzle repeats).  K (matrices: rows 0-7 and 8-15 of the group's first
     // half, then of its second): a lane gets the 8 dims 8c.. of row g, g + 8,
     // then the dims 32 + 8c...  V (transposed; token rows 0-7 of both halves,
     // then 8-15): a lane gets dims 4g.. of tokens 2c and 2c + 1 in one word.
@@ -778,8 +874,8 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const int r8 = lane & 7, m = lane >> 3;
 #pragma unroll
         for (int gr = 0; gr < C::kGroups; ++gr) {
-            k4_off[gr] = swz<C::kRowBytes, C::kSwizzle>(row0 + r8 + 8 * (m & 1), 32 * gr + 16 * (m >> 1));
-            v4_off[gr] = swz<C::kRowBytes, C::kSwizzle>(row0 + r8 + 8 * (m >> 1), 32 * gr + 16 * (m & 1));
+            k4_off[gr] = swz<C::kRowBytes, C::kSwizzle>(r8 + 8 * (m & 1), 32 * gr + 16 * (m >> 1));
+            v4_off[gr] = swz<C::kRowBytes, C::kSwizzle>(r8 + 8 * (m >> 1), 32 * gr + 16 * (m & 1));
         }
     }
 
@@ -1042,13 +1138,15 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 // (1) sum of q . code per group: a code in bits 0-3 (4-7) of an f16
                 // whose other bits are zero reads as the subnormal code * 2^-24
                 // (* 2^-20), exactly, so one AND makes an operand pair.
+                const uint32_t kb4 = smem_addr(smem + stage * C::kStageBytes);
+                const uint32_t vb4 = kb4 + C::kTileBytes;
                 float acc[kH][kNB][C::kGroups][4];
 #pragma unroll
                 for (int t = 0; t < kH; ++t) {
 #pragma unroll
                     for (int gr = 0; gr < C::kGroups; ++gr) {
                         uint32_t x[4];
-                        ldsm_x4(kb_head + k4_off[gr] + t * 16 * C::kRowBytes, x[0], x[1], x[2], x[3]);
+                        ldsm_x4(kb4 + k4_off[gr] + trow[t] * C::kRowBytes, x[0], x[1], x[2], x[3]);
 #pragma unroll
                         for (int nb = 0; nb < kNB; ++nb)
                             acc[t][nb][gr][0] = acc[t][nb][gr][1] = acc[t][nb][gr][2] =
@@ -1074,15 +1172,14 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 float p[kH][kNB][4];
                 float vs[kH][2][C::kGroups], vm[kH][2][C::kGroups];   // V's of rows g, g + 8
                 float vtop = 0.f, ptop = kNegInf;
-                const uint32_t par = smem_addr(smem + stage * C::kStageBytes) + 2 * C::kTileBytes +
-                                     (kvh_w * kChunkTokens + row0 + g) * kPR;
+                const uint32_t par = vb4 + C::kTileBytes + g * kPR;
 #pragma unroll
                 for (int t = 0; t < kH; ++t) {
                     float ks[2][C::kGroups];
                     uint32_t kw[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint32_t kp = par + (16 * t + 8 * i) * kPR, vp = kp + C::kParTileBytes;
+                        const uint32_t kp = par + (trow[t] + 8 * i) * kPR, vp = kp + C::kParTileBytes;
                         if constexpr (C::kGroups == 2) {
                             const uint2 x = lds64(kp), y = lds64(vp);
                             kw[i] = lds32(kp + 4 * (c & 1));
@@ -1217,7 +1314,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         // x[0], x[1]: tokens 2c, 2c+1, dims 4g.. of the halves; x[2], x[3]:
                         // tokens 8 + 2c, 8 + 2c + 1
                         uint32_t x[4];
-                        ldsm_x4_trans(vb_head + v4_off[gr] + t * 16 * C::kRowBytes, x[0], x[1], x[2], x[3]);
+                        ldsm_x4_trans(vb4 + v4_off[gr] + trow[t] * C::kRowBytes, x[0], x[1], x[2], x[3]);
 #pragma unroll
                         for (int half = 0; half < 2; ++half)
 #pragma unroll

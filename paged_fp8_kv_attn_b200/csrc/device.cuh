@@ -151,6 +151,18 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes
                  "r"(bytes)
                  : "memory");
 }
+// Copies 16 bytes to shared memory (both addresses 16-byte aligned), and an
+// arrival on the barrier once this thread's copies so far have landed (counted
+// like any arrival).
+__device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst),
+                 "l"(reinterpret_cast<uint64_t>(src))
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
 // Hint: bring the 128-byte line holding p into L2.
 __device__ __forceinline__ void prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));

@@ -56,7 +56,10 @@ struct AttnArgs {
     const int32_t* chunk_begin;  // [B]
     const float* pfx_ml;         // [items][G][4]
     const float* pfx_o;          // [items][G][D]
-    // INT4: the pools' (scale, minimum) pairs, [NP][Hkv][P][D/64][2] bf16.
+    // INT4: the pools' codes, [NP][Hkv][P][D/2], and (scale, minimum) pairs,
+    // [NP][Hkv][P][D/64][2] bf16.
+    const uint8_t* k_codes;
+    const uint8_t* v_codes;
     const uint8_t* k_params;
     const uint8_t* v_params;
     // Window: tokens t < sinks and t >= len - window are visible (window 0: all).
