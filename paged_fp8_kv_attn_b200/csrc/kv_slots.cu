@@ -1,104 +1,168 @@
 // kv_slots.cu -- token writes into cache slots named by a slot map, and reads
 // of such slots back as bf16, for FP8, BF16 and INT4 caches.
 //
-// One thread moves one 8-value block (16 bytes of bf16) of K and the same
-// block of V, so two loads are in flight per thread and each 128-byte line of
-// the token rows is read by 8 consecutive lanes; an INT4 group of 64 dims is
-// exactly those 8 lanes, whose minimum and maximum meet in three shuffles.
+// A warp moves the K rows or the V rows of `tokens` consecutive tokens, as many
+// as make kInFlight 8-value blocks (16 bytes of bf16) for each lane, at least
+// one: 32 consecutive blocks at a time are 512 bytes of one row, or whole short
+// rows, and an INT4 group of 64 dims is 8 consecutive lanes, whose minimum and
+// maximum meet in three shuffles.  Nothing is read twice, so memory bounds large
+// calls, and the chain of two dependent loads, slot then row, small ones: a
+// lane's kInFlight blocks are loaded together, and K and V are different warps.
 #include "kv_codec.cuh"
 
 namespace pkv {
 
 constexpr int kSlotThreads = 256;
+constexpr int kSlotWarps = kSlotThreads / 32;
+constexpr int kInFlight = 4;
 
-// Block of the calling thread: its token and the (head, 8-dim block) in the
-// token's row.  The blocks of `tokens_per_cta` consecutive tokens form a CTA's
-// work, kSlotThreads at a time (a row has a multiple of 8 blocks, so 8
-// consecutive lanes always share token and head).
-template <typename F>
-__device__ __forceinline__ void for_each_block(const SlotArgs& a, int tokens_per_cta, F f) {
-    const int row_blocks = a.num_kv_heads * (a.head_dim / 8);
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_cta;
-    const int64_t left = a.num_tokens - t0;
-    const int tokens = static_cast<int>(left < tokens_per_cta ? left : tokens_per_cta);
-    const int total = tokens * row_blocks;
-    const int64_t slots = static_cast<int64_t>(a.num_pages) * a.page_size;
-    for (int e = threadIdx.x; e < total; e += kSlotThreads) {
-        const int t = e / row_blocks;
-        const int r = e - t * row_blocks;
-        const int h = r / (a.head_dim / 8);
-        const int d8 = r - h * (a.head_dim / 8);
-        const int32_t slot = a.slot_map[t0 + t];
-        int64_t row = -1;
-        if (slot >= 0 && slot < slots) {
-            const int32_t page = slot / a.page_size;
-            row = (static_cast<int64_t>(page) * a.num_kv_heads + h) * a.page_size +
-                  (slot - page * a.page_size);
+// The calling warp's part of a call: blocks [0, total) of its tokens' rows.
+// kOne: a single token, whose slot is loaded and resolved once (measured: half
+// the time of a long row's write, 2 us of 10 of its read).
+template <int kD, bool kOne>
+struct SlotWork {
+    const SlotArgs& a;
+    int blocks;       // per row, a multiple of 8
+    uint32_t inv;     // ceil(2^16 / blocks)
+    int64_t token0;
+    int total;
+    bool is_v;
+    int shift;        // log2(page size)
+    int32_t row0;     // kOne: the token's pool row of head 0, negative without a slot
+
+    __device__ __forceinline__ SlotWork(const SlotArgs& args, int tokens)
+        : a(args), blocks(args.num_kv_heads * (kD / 8)) {
+        const int64_t w = static_cast<int64_t>(blockIdx.x) * kSlotWarps + (threadIdx.x >> 5);
+        is_v = (w & 1) != 0;
+        token0 = (w >> 1) * tokens;
+        const int64_t left = a.num_tokens - token0;
+        total = static_cast<int>(left < tokens ? (left > 0 ? left : 0) : tokens) * blocks;
+        inv = (65536u + blocks - 1) / blocks;
+        shift = 31 - __clz(a.page_size);
+        row0 = kOne && total > 0 ? row_of(a.slot_map[token0]) : -1;
+    }
+    // The token (from token0) of block u.  (tokens * blocks is at most 32 kInFlight,
+    // and u times inv's excess below 2^16.)
+    __device__ __forceinline__ int token_of(int u) const {
+        return kOne ? 0 : static_cast<int>((u * inv) >> 16);
+    }
+    // Pool row of a slot's head 0 (below 2^31); negative without a slot.
+    __device__ __forceinline__ int32_t row_of(int32_t slot) const {
+        if (slot < 0 || slot >= static_cast<int64_t>(a.num_pages) << shift) return -1;
+        return (((slot >> shift) * a.num_kv_heads) << shift) + (slot & (a.page_size - 1));
+    }
+    __device__ __forceinline__ int32_t load_row(int t) const {
+        return kOne ? row0 : row_of(a.slot_map[token0 + t]);
+    }
+    __device__ __forceinline__ int64_t head_row(int32_t row, int e) const {
+        return row + ((e / (kD / 8)) << shift);
+    }
+};
+
+template <int kKv, int kD, bool kOne>
+__global__ void __launch_bounds__(kSlotThreads)
+write_slots_kernel(const KvDst dst, const uint16_t* __restrict__ k_new,
+                   const uint16_t* __restrict__ v_new, const SlotArgs a, int tokens) {
+    launch_dependents();
+    grid_dependency_wait();
+    const SlotWork<kD, kOne> w(a, tokens);
+    if (kOne && w.row0 < 0) return;
+    const int64_t stride = w.is_v ? a.v_stride : a.k_stride;
+    const uint16_t* const src = (w.is_v ? v_new : k_new) + w.token0 * stride;
+    void* const cache = w.is_v ? dst.v : dst.k;
+    uint32_t* const params = w.is_v ? dst.v_params : dst.k_params;
+    const float scale = w.is_v ? dst.v_scale : dst.k_scale;
+    for (int u0 = threadIdx.x & 31; u0 < w.total; u0 += 32 * kInFlight) {
+        uint4 raw[kInFlight];
+        int32_t row[kInFlight];
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) {
+            const int u = u0 + 32 * i, t = w.token_of(u);
+            row[i] = u < w.total ? w.load_row(t) : -1;
         }
-        f(t0 + t, static_cast<int64_t>(r) * 8, row, d8);
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) {
+            const int u = u0 + 32 * i, t = w.token_of(u);
+            if (u < w.total && row[i] >= 0)
+                raw[i] = *reinterpret_cast<const uint4*>(src + t * stride + (u - t * w.blocks) * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) {
+            const int u = u0 + 32 * i, e = u - w.token_of(u) * w.blocks;
+            if (u < w.total && row[i] >= 0)
+                store8<kKv>(cache, params, w.head_row(row[i], e), kD, e % (kD / 8), raw[i], scale);
+        }
     }
 }
 
-template <int kKv>
-__global__ void __launch_bounds__(kSlotThreads)
-write_slots_kernel(const KvDst dst, const uint16_t* __restrict__ k_new,
-                   const uint16_t* __restrict__ v_new, const SlotArgs a, int tokens_per_cta) {
-    launch_dependents();
-    grid_dependency_wait();
-    for_each_block(a, tokens_per_cta, [&](int64_t t, int64_t off, int64_t row, int d8) {
-        if (row < 0) return;
-        const uint4 k = *reinterpret_cast<const uint4*>(k_new + t * a.k_stride + off);
-        const uint4 v = *reinterpret_cast<const uint4*>(v_new + t * a.v_stride + off);
-        store8<kKv>(dst.k, dst.k_params, row, a.head_dim, d8, k, dst.k_scale);
-        store8<kKv>(dst.v, dst.v_params, row, a.head_dim, d8, v, dst.v_scale);
-    });
-}
-
-template <int kKv>
+template <int kKv, int kD, bool kOne>
 __global__ void __launch_bounds__(kSlotThreads)
 read_slots_kernel(const KvDst src, uint16_t* __restrict__ k_out, uint16_t* __restrict__ v_out,
-                  const SlotArgs a, int tokens_per_cta) {
+                  const SlotArgs a, int tokens) {
     launch_dependents();
     grid_dependency_wait();
-    for_each_block(a, tokens_per_cta, [&](int64_t t, int64_t off, int64_t row, int d8) {
-        uint4 k = make_uint4(0, 0, 0, 0), v = k;
-        if (row >= 0) {
-            k = load8<kKv>(src.k, src.k_params, row, a.head_dim, d8, src.k_scale);
-            v = load8<kKv>(src.v, src.v_params, row, a.head_dim, d8, src.v_scale);
+    const SlotWork<kD, kOne> w(a, tokens);
+    const int64_t stride = w.is_v ? a.v_stride : a.k_stride;
+    uint16_t* const out = (w.is_v ? v_out : k_out) + w.token0 * stride;
+    const void* const cache = w.is_v ? src.v : src.k;
+    const uint32_t* const params = w.is_v ? src.v_params : src.k_params;
+    const float scale = w.is_v ? src.v_scale : src.k_scale;
+    for (int u0 = threadIdx.x & 31; u0 < w.total; u0 += 32 * kInFlight) {
+        Held8 raw[kInFlight];
+        int32_t row[kInFlight];
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) {
+            const int u = u0 + 32 * i, t = w.token_of(u);
+            row[i] = u < w.total ? w.load_row(t) : -1;
         }
-        *reinterpret_cast<uint4*>(k_out + t * a.k_stride + off) = k;
-        *reinterpret_cast<uint4*>(v_out + t * a.v_stride + off) = v;
-    });
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) {
+            const int u = u0 + 32 * i, e = u - w.token_of(u) * w.blocks;
+            if (row[i] >= 0)
+                raw[i] = load8<kKv>(cache, params, w.head_row(row[i], e), kD, e % (kD / 8));
+        }
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) {
+            const int u = u0 + 32 * i, t = w.token_of(u);
+            if (u < w.total)
+                *reinterpret_cast<uint4*>(out + t * stride + (u - t * w.blocks) * 8) =
+                    row[i] >= 0 ? decode8<kKv>(raw[i], scale) : make_uint4(0, 0, 0, 0);
+        }
+    }
 }
 
-// Tokens per CTA: one pass of the CTA's threads over its blocks, or one token
-// where a row has more.
-static int slot_tokens_per_cta(const SlotArgs& a) {
-    const int row_blocks = a.num_kv_heads * (a.head_dim / 8);
-    const int n = kSlotThreads / row_blocks;
-    return n < 1 ? 1 : n;
+// A warp takes as many whole rows as fill its lanes kInFlight times.
+static int slot_tokens(const SlotArgs& a) {
+    const int blocks = a.num_kv_heads * (a.head_dim / 8);
+    return blocks >= 32 * kInFlight ? 1 : 32 * kInFlight / blocks;
 }
+
+template <typename K, typename... A>
+static cudaError_t launch_slots(K kernel, const SlotArgs& a, cudaStream_t stream, A... args) {
+    const int tokens = slot_tokens(a);
+    const int64_t warps = 2 * ((static_cast<int64_t>(a.num_tokens) - 1) / tokens + 1);
+    PdlLaunch l(dim3(static_cast<unsigned>((warps - 1) / kSlotWarps + 1)), dim3(kSlotThreads), 0,
+                stream);
+    return cudaLaunchKernelEx(&l.cfg, kernel, args..., a, tokens);
+}
+
+#define PKV_SLOT_KERNEL(NAME, KV, D, ONE)                                                   \
+    (ONE ? PKV_SLOT_KERNEL_(NAME, KV, D, true) : PKV_SLOT_KERNEL_(NAME, KV, D, false))
+#define PKV_SLOT_KERNEL_(NAME, KV, D, ONE)                                                  \
+    (KV == kKvFp8    ? (D == 64 ? NAME<kKvFp8, 64, ONE> : NAME<kKvFp8, 128, ONE>)             \
+     : KV == kKvBf16 ? (D == 64 ? NAME<kKvBf16, 64, ONE> : NAME<kKvBf16, 128, ONE>)           \
+                     : (D == 64 ? NAME<kKvInt4, 64, ONE> : NAME<kKvInt4, 128, ONE>))
 
 cudaError_t launch_write_slots(const KvDst& dst, const uint16_t* k_new, const uint16_t* v_new,
                                const SlotArgs& a, cudaStream_t stream) {
-    const int per = slot_tokens_per_cta(a);
-    PdlLaunch l(dim3(static_cast<unsigned>((a.num_tokens - 1) / per + 1)), dim3(kSlotThreads), 0,
-                stream);
-    auto* kernel = dst.kv == kKvFp8    ? write_slots_kernel<kKvFp8>
-                   : dst.kv == kKvBf16 ? write_slots_kernel<kKvBf16>
-                                       : write_slots_kernel<kKvInt4>;
-    return cudaLaunchKernelEx(&l.cfg, kernel, dst, k_new, v_new, a, per);
+    return launch_slots(PKV_SLOT_KERNEL(write_slots_kernel, dst.kv, a.head_dim, slot_tokens(a) == 1), a, stream, dst,
+                        k_new, v_new);
 }
 
 cudaError_t launch_read_slots(const KvDst& src, uint16_t* k_out, uint16_t* v_out,
                               const SlotArgs& a, cudaStream_t stream) {
-    const int per = slot_tokens_per_cta(a);
-    PdlLaunch l(dim3(static_cast<unsigned>((a.num_tokens - 1) / per + 1)), dim3(kSlotThreads), 0,
-                stream);
-    auto* kernel = src.kv == kKvFp8    ? read_slots_kernel<kKvFp8>
-                   : src.kv == kKvBf16 ? read_slots_kernel<kKvBf16>
-                                       : read_slots_kernel<kKvInt4>;
-    return cudaLaunchKernelEx(&l.cfg, kernel, src, k_out, v_out, a, per);
+    return launch_slots(PKV_SLOT_KERNEL(read_slots_kernel, src.kv, a.head_dim, slot_tokens(a) == 1), a, stream, src,
+                        k_out, v_out);
 }
 
 }  // namespace pkv
