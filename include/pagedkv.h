@@ -303,7 +303,9 @@ PKV_API pkv_status kv_read_slots_int4(const int32_t* slot_map, int32_t num_token
  * num_pages; page_table and expected_tags [batch][max_pages]; slot_map
  * [max_tokens]; cu_tokens [batch + 1]; failed [batch] uint8.  Apart from
  * num_free_out the written arrays may not overlap the others.
- * page_size is 16, 32, 64 or 128, num_pages * page_size < 2^31.  One kernel.
+ * page_size is 16, 32, 64 or 128, num_pages * page_size < 2^31.  One kernel,
+ * which lets no kernel behind it on the stream start before it has finished:
+ * attention may follow at once.
  */
 PKV_API pkv_status kv_extend_tables(const int32_t* old_lens, const int32_t* new_lens, int32_t batch,
                             int32_t page_size, const int32_t* free_pages, int32_t free_capacity,

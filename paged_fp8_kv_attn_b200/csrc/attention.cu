@@ -79,7 +79,7 @@ struct AttnCfg {
     // resident warps matter more than depth (each CTA keeps up to kStages
     // chunks in flight), so the depth is the largest that still lets
     // kMinBlocks CTAs share an SM's 228 KB of shared memory.
-    static constexpr int kStages = kInt4 ? (kD == 128 ? (kH == 2 ? 3 : 6) : 6)
+    static constexpr int kStages = kInt4 ? (kD == 128 ? (kH == 2 ? 3 : (kGP == 8 ? 5 : 6)) : 6)
                                    : kFp8 ? (kD == 128 ? (kH == 2 ? 3 : 4) : (kH == 2 ? 3 : 6))
                                           : (kD == 128 ? 2 : 4);
     static constexpr int kMinBlocks = (kFp8 && kGP == 8 && kH == 1) || (kInt4 && kGP == 8) ? 3 : 2;

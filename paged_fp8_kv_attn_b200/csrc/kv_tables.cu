@@ -45,7 +45,9 @@ __global__ void __launch_bounds__(kTableThreads) extend_tables_kernel(const Tabl
     __shared__ int32_t s_old[kTableRows];
     __shared__ bool s_ok[kTableRows];
     __shared__ uint32_t s_warp[2][kTableThreads / 32];
-    launch_dependents();
+    // No launch_dependents(): attention reads the page table before it waits for
+    // the kernel in front of it, so no later kernel may start before the rows are
+    // written.
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ctas = gridDim.x, rank = blockIdx.x;   // the grid is one cluster
@@ -56,8 +58,8 @@ __global__ void __launch_bounds__(kTableThreads) extend_tables_kernel(const Tabl
 
     const bool wide = reinterpret_cast<uintptr_t>(a.slot_map) % 16 == 0;
     auto pages_of = [&](int32_t len) { return (static_cast<uint32_t>(len) + P - 1) >> shift; };
-    // the free stack's page for the i-th page of the call
-    auto stack_page = [&](uint32_t i) { return a.free_pages[num_free - 1 - static_cast<int32_t>(i)]; };
+    // the free stack's entry for the i-th page of the call
+    auto stack_entry = [&](uint32_t i) { return a.free_pages + (num_free - 1 - static_cast<int32_t>(i)); };
 
     uint32_t pages0 = 0, toks0 = 0;   // before the pass's first row
     uint32_t taken = 0;               // pages of the rows served so far
@@ -121,45 +123,52 @@ __global__ void __launch_bounds__(kTableThreads) extend_tables_kernel(const Tabl
             const int r = last_at_most(s_page, rows, i);
             const int64_t at = static_cast<int64_t>(r0 + r) * a.max_pages + pages_of(s_old[r]) +
                                (i - s_page[r]);
-            const int32_t page = stack_page(i);
+            const int32_t page = *stack_entry(i);
             a.page_table[at] = page;
             if (a.page_tags != nullptr && page >= 0 && page < a.num_pages)
                 a.expected_tags[at] = a.page_tags[page];
         }
 
-        // The pass's tokens, kTableTokens consecutive ones at a time.
+        // The pass's tokens, kTableTokens consecutive ones at a time: their rows and
+        // positions, then all their pages' loads, then the slots.  (Threads counted
+        // from the end: a small call's pages and tokens are then different warps.)
         const uint32_t end = min(toks1, static_cast<uint32_t>(a.max_tokens));
-        for (uint32_t g = toks0 / kTableTokens + rank * kTableThreads + tid; g * kTableTokens < end;
-             g += ctas * kTableThreads) {
+        for (uint32_t g = toks0 / kTableTokens + rank * kTableThreads + (kTableThreads - 1 - tid);
+             g * kTableTokens < end; g += ctas * kTableThreads) {
             const uint32_t t0 = max(g * kTableTokens, toks0), t1 = min((g + 1) * kTableTokens, end);
-            int32_t slot[kTableTokens];
+            if (t0 >= t1) break;
+            const int32_t* from[kTableTokens];   // where a token's page id stands (null: no page)
+            int32_t page[kTableTokens], pos[kTableTokens];
             int r = last_at_most(s_tok, rows, t0);
-            int page_at = -1;       // the row's page-table position that `page` holds
-            int32_t page = -1;
-            for (uint32_t t = t0; t < t1; ++t) {
-                while (t >= s_tok[r + 1]) {
-                    ++r;
-                    page_at = -1;
-                }
-                int32_t s = -1;
-                if (s_ok[r]) {
-                    const int32_t pos = s_old[r] + static_cast<int32_t>(t - s_tok[r]);
-                    const int j = pos >> shift;
-                    if (j != page_at) {
-                        const int first = pages_of(s_old[r]);
-                        page = j >= first ? stack_page(s_page[r] + (j - first))
-                                          : a.page_table[static_cast<int64_t>(r0 + r) * a.max_pages + j];
-                        page_at = j;
-                    }
-                    if (page >= 0 && page < a.num_pages) s = page * P + (pos & (P - 1));
-                }
-                slot[t % kTableTokens] = s;
+#pragma unroll
+            for (int k = 0; k < kTableTokens; ++k) {
+                const uint32_t t = g * kTableTokens + k;
+                from[k] = nullptr;
+                if (t < t0 || t >= t1) continue;
+                while (t >= s_tok[r + 1]) ++r;
+                if (!s_ok[r]) continue;
+                const int32_t old = s_old[r];
+                pos[k] = old + static_cast<int32_t>(t - s_tok[r]);
+                const int j = pos[k] >> shift, first = pages_of(old);
+                from[k] = j >= first ? stack_entry(s_page[r] + (j - first))
+                                     : a.page_table + static_cast<int64_t>(r0 + r) * a.max_pages + j;
             }
-            if (wide && t1 - t0 == kTableTokens)
+#pragma unroll
+            for (int k = 0; k < kTableTokens; ++k) page[k] = from[k] != nullptr ? *from[k] : -1;
+            int32_t slot[kTableTokens];
+#pragma unroll
+            for (int k = 0; k < kTableTokens; ++k)
+                slot[k] = page[k] >= 0 && page[k] < a.num_pages ? page[k] * P + (pos[k] & (P - 1)) : -1;
+            if (wide && t1 - t0 == kTableTokens) {
                 *reinterpret_cast<int4*>(a.slot_map + t0) =
                     make_int4(slot[0], slot[1], slot[2], slot[3]);
-            else
-                for (uint32_t t = t0; t < t1; ++t) a.slot_map[t] = slot[t % kTableTokens];
+            } else {
+#pragma unroll
+                for (int k = 0; k < kTableTokens; ++k) {
+                    const uint32_t t = g * kTableTokens + k;
+                    if (t >= t0 && t < t1) a.slot_map[t] = slot[k];
+                }
+            }
         }
         pages0 = pages1;
         toks0 = toks1;
@@ -168,6 +177,7 @@ __global__ void __launch_bounds__(kTableThreads) extend_tables_kernel(const Tabl
     for (int64_t t = static_cast<int64_t>(toks0) + rank * kTableThreads + tid; t < a.max_tokens;
          t += ctas * kTableThreads)
         a.slot_map[t] = -1;
+    __threadfence();      // (a kernel that starts on this one's end sees the rows)
     cluster_sync_all();   // every CTA has read num_free
     if (rank == 0 && tid == 0) {
         a.cu_tokens[0] = 0;

@@ -610,3 +610,51 @@ def test_binding_refuses(cuda_device):
     with pytest.raises(ValueError, match="together"):
         run_tables(np.zeros(1, np.int32), np.ones(1, np.int32), 16, np.zeros(1, np.int32), 1,
                    np.zeros((1, 1), np.int32), 4, 1, tags=np.zeros(4, np.uint32))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("between", [False, True])
+def test_attention_sees_the_tables_of_the_call_before(cuda_device, kind, between):
+    """Tables, (a slot write,) and attention back to back, with no synchronisation: the
+    attention kernel may be scheduled early but must not read rows from before.  Both
+    of two states are attended to in turn, and compared with the same call made alone."""
+    B, H, D, P, NP = 48, 2, 64, 16, 1600
+    rng = np.random.Generator(np.random.PCG64(2))
+    p = ref.Pools(kind, NP, H, P, D, 0.1, 0.1, seed=11)
+    c = Cache(p)
+    old, new = np.zeros(B, np.int32), rng.integers(300, 500, B).astype(np.int32)
+    MP, T = 32, int(new.sum())
+    assert -(-new // P).sum() <= NP
+    stacks = [cuda(rng.permutation(NP).astype(np.int32)) for _ in range(2)]
+    nf, nfo = (torch.tensor([NP], dtype=torch.int32, device="cuda") for _ in range(2))
+    table = torch.full((B, MP), -1, dtype=torch.int32, device="cuda")
+    slots = torch.zeros(T, dtype=torch.int32, device="cuda")
+    cu_tokens, failed = torch.zeros(B + 1, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.uint8, device="cuda")
+    g_old, g_new, q = cuda(old), cuda(new), cuda(normal_bits(rng, (B, 2 * H, D)))
+    rows = torch.zeros((1, H, D), dtype=torch.bfloat16, device="cuda")
+    nowhere = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    ws = c.workspace(B, 2 * H)
+
+    def tables(i):
+        pkv.kv_extend_tables(g_old, g_new, P, stacks[i], nf, table, slots, cu_tokens, failed, nfo, NP)
+
+    want = []
+    for i in range(2):
+        tables(i)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in c.attend(q, table, g_new, 0.1, ws)])
+        torch.cuda.synchronize()
+    outs = [tuple(torch.zeros_like(t) for t in want[0]) for _ in range(40)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()   # (replayed, the kernels follow one another at once)
+    with torch.cuda.graph(graph):
+        for n, out in enumerate(outs):
+            tables(n % 2)
+            if between:
+                c.write(rows, rows, nowhere)
+            c.attend(q, table, g_new, 0.1, ws, out=out)
+    graph.replay()
+    torch.cuda.synchronize()
+    for n, out in enumerate(outs):
+        for got, w in zip(out, want[n % 2]):
+            assert torch.equal(got, w), f"call {n}"
