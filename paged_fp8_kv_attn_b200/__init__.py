@@ -178,12 +178,22 @@ def _need(t, dtype, ndim, name):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _vector(t, n, dtype, name):
-    """Address of a vector of n entries."""
-    _need(t, dtype, 1, name)
-    if t.numel() != n:
-        raise ValueError(f"{name} must be ({n},), got {tuple(t.shape)}")
-    return t.data_ptr()
+def _on(stream):
+    """Device index and stream handle of a call."""
+    if stream is None:
+        dev = torch.cuda.current_device()
+        return dev, _raw_stream(dev)
+    return stream.device_index, stream.cuda_stream
+
+
+def _args(dev, *specs):
+    """Each (name, tensor, dtype, shape): contiguous, on the call's device."""
+    for name, t, dtype, shape in specs:
+        if t is None or t.get_device() != dev or t.dtype is not dtype or t.shape != shape \
+                or not t.is_contiguous():
+            _need(t, dtype, len(shape), name)
+            _match(name, t, shape)
+            raise ValueError(f"{name} must be on the call's device {dev}, got {t.device}")
 
 
 def _match(name, t, shape):
@@ -191,31 +201,27 @@ def _match(name, t, shape):
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _here(stream, *tensors):
-    """The call runs on the current device: refuses tensors of another one."""
-    dev = torch.cuda.current_device() if stream is None else stream.device_index
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors must be on the call's device {dev}, got {t.device}")
+def _tag_dtype(t, name):
+    """The dtype of tags: one of _TAG_DTYPES."""
+    return _need(t, _TAG_DTYPES, 1, name).dtype
 
 
-def _int4_pools(k_codes, k_params, v_codes, v_params):
-    """(NP, Hkv, P, D) of an INT4 cache."""
-    _need(k_codes, torch.uint8, 4, "k_codes")
-    shape = k_codes.shape
-    NP, Hkv, P, half = shape
-    par = (NP, Hkv, P, 2 * half // INT4_GROUP, 2)
-    _match("v_codes", _need(v_codes, torch.uint8, 4, "v_codes"), shape)
-    _match("k_params", _need(k_params, torch.bfloat16, 5, "k_params"), par)
-    _match("v_params", _need(v_params, torch.bfloat16, 5, "v_params"), par)
+def _int4_shape(k_codes):
+    """(NP, Hkv, P, D) of an INT4 cache with these K codes."""
+    NP, Hkv, P, half = _need(k_codes, torch.uint8, 4, "k_codes").shape
     return NP, Hkv, P, 2 * half
 
 
-def _pools(k_cache, v_cache, dtype):
-    """(NP, Hkv, P, D) of an FP8 or BF16 cache."""
-    _need(k_cache, dtype, 4, "k_cache")
-    _match("v_cache", _need(v_cache, dtype, 4, "v_cache"), k_cache.shape)
-    return tuple(k_cache.shape)
+def _int4_specs(shape, k_codes, k_params, v_codes, v_params):
+    NP, Hkv, P, D = shape
+    codes, params = (NP, Hkv, P, D // 2), (NP, Hkv, P, D // INT4_GROUP, 2)
+    return (("k_codes", k_codes, torch.uint8, codes), ("k_params", k_params, torch.bfloat16, params),
+            ("v_codes", v_codes, torch.uint8, codes), ("v_params", v_params, torch.bfloat16, params))
+
+
+def _pool_specs(shape, dtype, k_cache, v_cache):
+    """Of an FP8 or BF16 cache."""
+    return ("k_cache", k_cache, dtype, shape), ("v_cache", v_cache, dtype, shape)
 
 
 _TAG_DTYPES = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
@@ -241,22 +247,19 @@ def kv_tag_check_window(page_tags, page_table, expected_tags, seq_lens, page_siz
                         abort_out, num_aborted=None, stream=None):
     """kv_tag_check of the pages that hold one of the last `window` or the first
     `sinks` tokens of a request; entries of hidden pages are not read."""
-    _need(page_tags, _TAG_DTYPES, 1, "page_tags")
-    _need(page_table, torch.int32, 2, "page_table")
-    _need(expected_tags, _TAG_DTYPES, 2, "expected_tags")
-    _need(seq_lens, torch.int32, 1, "seq_lens")
-    _need(abort_out, torch.uint8, 1, "abort_out")
-    B, MP = page_table.shape
-    _match("expected_tags", expected_tags, (B, MP))
-    _match("seq_lens", seq_lens, (B,))
-    _match("abort_out", abort_out, (B,))
+    i32 = torch.int32
+    B, MP = _need(page_table, i32, 2, "page_table").shape
+    tag = _tag_dtype(page_tags, "page_tags")
+    dev, handle = _on(stream)
+    _args(dev, ("page_tags", page_tags, tag, page_tags.shape), ("page_table", page_table, i32, (B, MP)),
+          ("expected_tags", expected_tags, tag, (B, MP)), ("seq_lens", seq_lens, i32, (B,)),
+          ("abort_out", abort_out, torch.uint8, (B,)))
     if num_aborted is not None:
-        _need(num_aborted, torch.int32, 1, "num_aborted")
-    _here(stream, page_tags, page_table, expected_tags, seq_lens, abort_out, num_aborted)
+        _args(dev, ("num_aborted", num_aborted, i32, (1,)))
     _check("kv_tag_check_window", _load().kv_tag_check_window(
         _ptr(page_tags), page_tags.shape[0], _ptr(page_table), _ptr(expected_tags), MP,
         _ptr(seq_lens), B, page_size, int(window), int(sinks), _ptr(abort_out), _ptr(num_aborted),
-        _stream(stream)))
+        handle))
 
 
 def kv_retag_pages(page_tags, pages, stream=None):
@@ -364,113 +367,117 @@ def kv_check_append_bf16(page_tags, page_table, expected_tags, seq_lens, page_si
 def kv_append_int4(k_new, v_new, page_table, seq_lens, page_size, k_codes, k_params, v_codes,
                    v_params, abort=None, stream=None):
     """Quantise each request's new K/V token to 4 bits and write it into its page."""
-    NP, Hkv, P, D = _int4_pools(k_codes, k_params, v_codes, v_params)
-    B = _new_tokens(k_new, v_new, page_table, seq_lens, Hkv, P, D, page_size)
+    shape = NP, Hkv, P, D = _int4_shape(k_codes)
+    B, MP = _need(page_table, torch.int32, 2, "page_table").shape
+    dev, handle = _on(stream)
+    _args(dev, *_int4_specs(shape, k_codes, k_params, v_codes, v_params),
+          *_append_specs(k_new, v_new, page_table, seq_lens, page_size, shape, B, MP))
     if abort is not None:
-        _match("abort", _need(abort, torch.uint8, 1, "abort"), (B,))
-    _here(stream, k_new, v_new, page_table, seq_lens, k_codes, k_params, v_codes, v_params, abort)
+        _args(dev, ("abort", abort, torch.uint8, (B,)))
     _check("kv_append_int4", _load().kv_append_int4(
-        _ptr(k_new), _ptr(v_new), _ptr(page_table), page_table.shape[1], _ptr(seq_lens), B, Hkv,
-        D, page_size, _ptr(k_codes), _ptr(k_params), _ptr(v_codes), _ptr(v_params), NP,
-        _ptr(abort), _stream(stream)))
+        _ptr(k_new), _ptr(v_new), _ptr(page_table), MP, _ptr(seq_lens), B, Hkv, D, P,
+        _ptr(k_codes), _ptr(k_params), _ptr(v_codes), _ptr(v_params), NP, _ptr(abort), handle))
 
 
 def kv_check_append_int4(page_tags, page_table, expected_tags, seq_lens, page_size, k_new, v_new,
                          k_codes, k_params, v_codes, v_params, abort_out, num_aborted=None,
                          stream=None):
     """kv_tag_check then kv_append_int4 (with that abort mask) in one kernel."""
-    NP, Hkv, P, D = _int4_pools(k_codes, k_params, v_codes, v_params)
-    B = _new_tokens(k_new, v_new, page_table, seq_lens, Hkv, P, D, page_size)
-    _match("page_tags", _need(page_tags, _TAG_DTYPES, 1, "page_tags"), (NP,))
-    _match("expected_tags", _need(expected_tags, _TAG_DTYPES, 2, "expected_tags"), page_table.shape)
-    _match("abort_out", _need(abort_out, torch.uint8, 1, "abort_out"), (B,))
+    shape = NP, Hkv, P, D = _int4_shape(k_codes)
+    B, MP = _need(page_table, torch.int32, 2, "page_table").shape
+    tag = _tag_dtype(page_tags, "page_tags")
+    dev, handle = _on(stream)
+    _args(dev, *_int4_specs(shape, k_codes, k_params, v_codes, v_params),
+          *_append_specs(k_new, v_new, page_table, seq_lens, page_size, shape, B, MP),
+          ("page_tags", page_tags, tag, (NP,)), ("expected_tags", expected_tags, tag, (B, MP)),
+          ("abort_out", abort_out, torch.uint8, (B,)))
     if num_aborted is not None:
-        _need(num_aborted, torch.int32, 1, "num_aborted")
-    _here(stream, page_tags, expected_tags, k_new, v_new, page_table, seq_lens, k_codes, k_params,
-          v_codes, v_params, abort_out, num_aborted)
+        _args(dev, ("num_aborted", num_aborted, torch.int32, (1,)))
     _check("kv_check_append_int4", _load().kv_check_append_int4(
-        _ptr(page_tags), NP, _ptr(page_table), _ptr(expected_tags), page_table.shape[1],
-        _ptr(seq_lens), B, page_size, _ptr(k_new), _ptr(v_new), Hkv, D, _ptr(k_codes),
-        _ptr(k_params), _ptr(v_codes), _ptr(v_params), _ptr(abort_out), _ptr(num_aborted),
-        _stream(stream)))
+        _ptr(page_tags), NP, _ptr(page_table), _ptr(expected_tags), MP, _ptr(seq_lens), B, P,
+        _ptr(k_new), _ptr(v_new), Hkv, D, _ptr(k_codes), _ptr(k_params), _ptr(v_codes),
+        _ptr(v_params), _ptr(abort_out), _ptr(num_aborted), handle))
 
 
-def _new_tokens(k_new, v_new, page_table, seq_lens, Hkv, P, D, page_size):
-    """The batch of an append to a cache of [Hkv][P][D] pages."""
-    _need(k_new, torch.bfloat16, 3, "k_new")
-    _need(page_table, torch.int32, 2, "page_table")
-    B = page_table.shape[0]
-    _match("k_new", k_new, (B, Hkv, D))
-    _match("v_new", _need(v_new, torch.bfloat16, 3, "v_new"), (B, Hkv, D))
-    _match("seq_lens", _need(seq_lens, torch.int32, 1, "seq_lens"), (B,))
+def _append_specs(k_new, v_new, page_table, seq_lens, page_size, shape, B, MP):
+    """Of an append to a cache of that shape."""
+    _, Hkv, P, D = shape
     if page_size != P:
         raise ValueError(f"page_size is {page_size}, the cache's pages hold {P} tokens")
-    return B
+    return (("k_new", k_new, torch.bfloat16, (B, Hkv, D)), ("v_new", v_new, torch.bfloat16, (B, Hkv, D)),
+            ("page_table", page_table, torch.int32, (B, MP)), ("seq_lens", seq_lens, torch.int32, (B,)))
 
 
-def _token_rows(t, name, T, Hkv, D):
+def _token_rows(t, name, T, Hkv, D, dev):
     """Row stride of [T][Hkv][D] token rows, each row contiguous."""
-    if t is None or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t is None or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
     _match(name, t, (T, Hkv, D))
-    row, stride = Hkv * D, t.stride()
-    if T < 2:
-        stride = (row, *stride[1:])
-    if T and (stride[2] != 1 or (Hkv > 1 and stride[1] != D) or stride[0] < row):
+    row = Hkv * D
+    if T < 2 and t.is_contiguous():
+        return row
+    stride = t.stride()
+    if T and (stride[2] != 1 or (Hkv > 1 and stride[1] != D) or (T > 1 and stride[0] < row)):
         raise ValueError(f"{name} must hold each token's [Hkv][D] values contiguously")
-    return stride[0]
+    return stride[0] if T > 1 else row
 
 
-def _slot_call(name, slot_map, pools, scales, k, v, shape, write, stream):
+def _slot_call(name, slot_map, pools, scales, k, v, shape, specs, write, stream):
     T = _need(slot_map, torch.int32, 1, "slot_map").numel()
     NP, Hkv, P, D = shape
-    ks, vs = _token_rows(k, "k", T, Hkv, D), _token_rows(v, "v", T, Hkv, D)
-    _here(stream, slot_map, *pools, k, v)
+    dev, handle = _on(stream)
+    _args(dev, *specs, ("slot_map", slot_map, torch.int32, (T,)))
+    ks, vs = _token_rows(k, "k", T, Hkv, D, dev), _token_rows(v, "v", T, Hkv, D, dev)
     rows = (k.data_ptr(), v.data_ptr(), ks, vs)
     cache = (slot_map.data_ptr(), T, Hkv, D, P, *scales, *[t.data_ptr() for t in pools], NP)
     fn = getattr(_load(), name)
-    _check(name, fn(*rows, *cache, _stream(stream)) if write else
-           fn(*cache, *rows, _stream(stream)))
+    _check(name, fn(*rows, *cache, handle) if write else fn(*cache, *rows, handle))
 
 
 def kv_write_slots_fp8(k_new, v_new, slot_map, k_scale, v_scale, k_cache, v_cache, stream=None):
     """Quantise token rows to E4M3 and write row i into slot slot_map[i] (negative: skipped)."""
+    shape = _need(k_cache, torch.uint8, 4, "k_cache").shape
     _slot_call("kv_write_slots_fp8", slot_map, (k_cache, v_cache), (float(k_scale), float(v_scale)),
-               k_new, v_new, _pools(k_cache, v_cache, torch.uint8), True, stream)
+               k_new, v_new, shape, _pool_specs(shape, torch.uint8, k_cache, v_cache), True, stream)
 
 
 def kv_write_slots_bf16(k_new, v_new, slot_map, k_cache, v_cache, stream=None):
     """Write token row i into slot slot_map[i] of a BF16 cache (negative: skipped)."""
-    _slot_call("kv_write_slots_bf16", slot_map, (k_cache, v_cache), (), k_new, v_new,
-               _pools(k_cache, v_cache, torch.bfloat16), True, stream)
+    shape = _need(k_cache, torch.bfloat16, 4, "k_cache").shape
+    _slot_call("kv_write_slots_bf16", slot_map, (k_cache, v_cache), (), k_new, v_new, shape,
+               _pool_specs(shape, torch.bfloat16, k_cache, v_cache), True, stream)
 
 
 def kv_write_slots_int4(k_new, v_new, slot_map, k_codes, k_params, v_codes, v_params, stream=None):
     """Quantise token rows to 4 bits and write row i into slot slot_map[i] (negative: skipped)."""
     pools = (k_codes, k_params, v_codes, v_params)
-    _slot_call("kv_write_slots_int4", slot_map, pools, (), k_new, v_new, _int4_pools(*pools), True,
-               stream)
+    shape = _int4_shape(k_codes)
+    _slot_call("kv_write_slots_int4", slot_map, pools, (), k_new, v_new, shape,
+               _int4_specs(shape, *pools), True, stream)
 
 
 def kv_read_slots_fp8(slot_map, k_scale, v_scale, k_cache, v_cache, k_out, v_out, stream=None):
     """The bf16 values of the slots that slot_map names (zeros for none) of an E4M3 cache."""
+    shape = _need(k_cache, torch.uint8, 4, "k_cache").shape
     _slot_call("kv_read_slots_fp8", slot_map, (k_cache, v_cache), (float(k_scale), float(v_scale)),
-               k_out, v_out, _pools(k_cache, v_cache, torch.uint8), False, stream)
+               k_out, v_out, shape, _pool_specs(shape, torch.uint8, k_cache, v_cache), False, stream)
 
 
 def kv_read_slots_bf16(slot_map, k_cache, v_cache, k_out, v_out, stream=None):
     """The values of the slots that slot_map names (zeros for none) of a BF16 cache."""
-    _slot_call("kv_read_slots_bf16", slot_map, (k_cache, v_cache), (), k_out, v_out,
-               _pools(k_cache, v_cache, torch.bfloat16), False, stream)
+    shape = _need(k_cache, torch.bfloat16, 4, "k_cache").shape
+    _slot_call("kv_read_slots_bf16", slot_map, (k_cache, v_cache), (), k_out, v_out, shape,
+               _pool_specs(shape, torch.bfloat16, k_cache, v_cache), False, stream)
 
 
 def kv_read_slots_int4(slot_map, k_codes, k_params, v_codes, v_params, k_out, v_out, stream=None):
     """The bf16 values of the slots that slot_map names (zeros for none) of an INT4 cache."""
     pools = (k_codes, k_params, v_codes, v_params)
-    _slot_call("kv_read_slots_int4", slot_map, pools, (), k_out, v_out, _int4_pools(*pools), False,
-               stream)
+    shape = _int4_shape(k_codes)
+    _slot_call("kv_read_slots_int4", slot_map, pools, (), k_out, v_out, shape,
+               _int4_specs(shape, *pools), False, stream)
 
 
 def kv_extend_tables(old_lens, new_lens, page_size, free_pages, num_free, page_table, slot_map,
@@ -482,22 +489,25 @@ def kv_extend_tables(old_lens, new_lens, page_size, free_pages, num_free, page_t
     (which may be num_free)."""
     i32 = torch.int32
     B, MP = _need(page_table, i32, 2, "page_table").shape
-    tags = expected = None
+    T = _need(slot_map, i32, 1, "slot_map").numel()
+    cap = _need(free_pages, i32, 1, "free_pages").numel()
+    dev, handle = _on(stream)
+    _args(dev, ("old_lens", old_lens, i32, (B,)), ("new_lens", new_lens, i32, (B,)),
+          ("free_pages", free_pages, i32, (cap,)), ("num_free", num_free, i32, (1,)),
+          ("num_free_out", num_free_out, i32, (1,)), ("page_table", page_table, i32, (B, MP)),
+          ("slot_map", slot_map, i32, (T,)), ("cu_tokens", cu_tokens, i32, (B + 1,)),
+          ("failed", failed, torch.uint8, (B,)))
     if page_tags is not None or expected_tags is not None:
         if page_tags is None or expected_tags is None:
             raise ValueError("page_tags and expected_tags are given together or not at all")
-        tags = _vector(page_tags, num_pages, _TAG_DTYPES, "page_tags")
-        _match("expected_tags", _need(expected_tags, _TAG_DTYPES, 2, "expected_tags"), (B, MP))
-        expected = expected_tags.data_ptr()
-    T, cap = _need(slot_map, i32, 1, "slot_map").numel(), _need(free_pages, i32, 1, "free_pages").numel()
-    args = (_vector(old_lens, B, i32, "old_lens"), _vector(new_lens, B, i32, "new_lens"), B,
-            int(page_size), free_pages.data_ptr(), cap, _vector(num_free, 1, i32, "num_free"),
-            _vector(num_free_out, 1, i32, "num_free_out"), int(num_pages), page_table.data_ptr(), MP,
-            tags, expected, slot_map.data_ptr(), T, _vector(cu_tokens, B + 1, i32, "cu_tokens"),
-            _vector(failed, B, torch.uint8, "failed"))
-    _here(stream, old_lens, new_lens, free_pages, num_free, num_free_out, page_table, page_tags,
-          expected_tags, slot_map, cu_tokens, failed)
-    _check("kv_extend_tables", _load().kv_extend_tables(*args, _stream(stream)))
+        tag = _tag_dtype(page_tags, "page_tags")
+        _args(dev, ("page_tags", page_tags, tag, (num_pages,)),
+              ("expected_tags", expected_tags, tag, (B, MP)))
+    _check("kv_extend_tables", _load().kv_extend_tables(
+        old_lens.data_ptr(), new_lens.data_ptr(), B, int(page_size), free_pages.data_ptr(), cap,
+        num_free.data_ptr(), num_free_out.data_ptr(), int(num_pages), page_table.data_ptr(), MP,
+        _ptr(page_tags), _ptr(expected_tags), slot_map.data_ptr(), T, cu_tokens.data_ptr(),
+        failed.data_ptr(), handle))
 
 
 def kv_requant_pages_fp8(src_pool, src_pages, dst_pool, dst_pages, scale, stream=None):
@@ -519,16 +529,16 @@ def kv_requant_pages_fp8(src_pool, src_pages, dst_pool, dst_pages, scale, stream
 def kv_requant_pages_int4(src_pool, src_pages, dst_codes, dst_params, dst_pages, stream=None):
     """BF16 -> INT4 page handoff: page src_pages[i] -> dst_pages[i]."""
     NPs, Hkv, P, D = _need(src_pool, torch.bfloat16, 4, "src_pool").shape
-    _need(src_pages, torch.int32, 1, "src_pages")
-    _match("dst_pages", _need(dst_pages, torch.int32, 1, "dst_pages"), src_pages.shape)
+    N = _need(src_pages, torch.int32, 1, "src_pages").numel()
     NPd = _need(dst_codes, torch.uint8, 4, "dst_codes").shape[0]
-    _match("dst_codes", dst_codes, (NPd, Hkv, P, D // 2))
-    _match("dst_params", _need(dst_params, torch.bfloat16, 5, "dst_params"),
-           (NPd, Hkv, P, D // INT4_GROUP, 2))
-    _here(stream, src_pool, src_pages, dst_codes, dst_params, dst_pages)
+    dev, handle = _on(stream)
+    _args(dev, ("src_pool", src_pool, torch.bfloat16, (NPs, Hkv, P, D)),
+          ("src_pages", src_pages, torch.int32, (N,)), ("dst_pages", dst_pages, torch.int32, (N,)),
+          ("dst_codes", dst_codes, torch.uint8, (NPd, Hkv, P, D // 2)),
+          ("dst_params", dst_params, torch.bfloat16, (NPd, Hkv, P, D // INT4_GROUP, 2)))
     _check("kv_requant_pages_int4", _load().kv_requant_pages_int4(
         _ptr(src_pool), NPs, _ptr(src_pages), _ptr(dst_codes), _ptr(dst_params), NPd,
-        _ptr(dst_pages), src_pages.shape[0], Hkv, P, D, _stream(stream)))
+        _ptr(dst_pages), N, Hkv, P, D, handle))
 
 
 def paged_decode_attn_workspace_size(kv_dtype, batch, num_q_heads, num_kv_heads, head_dim,
@@ -647,53 +657,56 @@ def paged_decode_attn_bf16(q, k_cache, v_cache, page_table, seq_lens, sm_scale, 
         _ptr(workspace), workspace.numel(), num_ctas, _stream(stream)))
 
 
-def _attn_call(name, pools, scales, shape, q, page_table, seq_lens, sm_scale, window, out, lse, workspace,
-               abort, num_ctas, stream):
+def _attn_call(name, pools, scales, shape, specs, q, page_table, seq_lens, sm_scale, window, out,
+               lse, workspace, abort, num_ctas, stream):
     """One attention call over a cache of `shape` = (NP, Hkv, P, D); pools are its
-    tensors, scales those of FP8 pools, window the (window, sinks) pair or ()."""
+    tensors (specs: as _args takes them), scales those of FP8 pools, window the
+    (window, sinks) pair or ()."""
     NP, Hkv, P, D = shape
-    _need(q, torch.bfloat16, 3, "q")
-    B, Hq, Dq = q.shape
+    B, Hq, Dq = _need(q, torch.bfloat16, 3, "q").shape
     if Dq != D:
         raise ValueError("head_dim of q and cache differ")
-    if _need(page_table, torch.int32, 2, "page_table").shape[0] != B:
-        raise ValueError("page_table must have a row per request")
-    _match("seq_lens", _need(seq_lens, torch.int32, 1, "seq_lens"), (B,))
-    _match("out", _need(out, torch.bfloat16, 3, "out"), (B, Hq, D))
-    _match("lse", _need(lse, torch.float32, 2, "lse"), (B, Hq))
-    _need(workspace, torch.uint8, 1, "workspace")
+    MP = _need(page_table, torch.int32, 2, "page_table").shape[1]
+    ws = _need(workspace, torch.uint8, 1, "workspace").numel()
+    dev, handle = _on(stream)
+    _args(dev, *specs, ("q", q, torch.bfloat16, (B, Hq, D)),
+          ("page_table", page_table, torch.int32, (B, MP)), ("seq_lens", seq_lens, torch.int32, (B,)),
+          ("out", out, torch.bfloat16, (B, Hq, D)), ("lse", lse, torch.float32, (B, Hq)),
+          ("workspace", workspace, torch.uint8, (ws,)))
     if abort is not None:
-        _match("abort", _need(abort, torch.uint8, 1, "abort"), (B,))
-    _here(stream, q, *pools, page_table, seq_lens, out, lse, workspace, abort)
+        _args(dev, ("abort", abort, torch.uint8, (B,)))
     _check(name, getattr(_load(), name)(
-        _ptr(q), *map(_ptr, pools), *scales, _ptr(page_table), page_table.shape[1], _ptr(seq_lens), B, Hq, Hkv, D, P,
-        NP, float(sm_scale), *window, _ptr(abort), _ptr(out), _ptr(lse), _ptr(workspace),
-        workspace.numel(), num_ctas, _stream(stream)))
+        q.data_ptr(), *[t.data_ptr() for t in pools], *scales, page_table.data_ptr(), MP,
+        seq_lens.data_ptr(), B, Hq, Hkv, D, P, NP, float(sm_scale), *window, _ptr(abort),
+        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ws, num_ctas, handle))
 
 
 def paged_decode_attn_int4(q, k_codes, k_params, v_codes, v_params, page_table, seq_lens, sm_scale,
                            out, lse, workspace, abort=None, num_ctas=0, stream=None):
     """Decode attention over a paged INT4 cache; writes out (bf16) and lse (fp32)."""
     pools = (k_codes, k_params, v_codes, v_params)
-    _attn_call("paged_decode_attn_int4", pools, (), _int4_pools(*pools), q, page_table, seq_lens,
-               sm_scale, (), out, lse, workspace, abort, num_ctas, stream)
+    shape = _int4_shape(k_codes)
+    _attn_call("paged_decode_attn_int4", pools, (), shape, _int4_specs(shape, *pools), q, page_table,
+               seq_lens, sm_scale, (), out, lse, workspace, abort, num_ctas, stream)
 
 
 def paged_decode_attn_fp8_window(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens,
                                  sm_scale, window, sinks, out, lse, workspace, abort=None,
                                  num_ctas=0, stream=None):
     """paged_decode_attn_fp8 over the last `window` and the first `sinks` tokens."""
+    shape = _need(k_cache, torch.uint8, 4, "k_cache").shape
     _attn_call("paged_decode_attn_fp8_window", (k_cache, v_cache), (float(k_scale), float(v_scale)),
-               _pools(k_cache, v_cache, torch.uint8), q, page_table, seq_lens, sm_scale,
-               (int(window), int(sinks)), out, lse, workspace, abort, num_ctas, stream)
+               shape, _pool_specs(shape, torch.uint8, k_cache, v_cache), q, page_table, seq_lens,
+               sm_scale, (int(window), int(sinks)), out, lse, workspace, abort, num_ctas, stream)
 
 
 def paged_decode_attn_bf16_window(q, k_cache, v_cache, page_table, seq_lens, sm_scale, window,
                                   sinks, out, lse, workspace, abort=None, num_ctas=0, stream=None):
     """paged_decode_attn_bf16 over the last `window` and the first `sinks` tokens."""
-    _attn_call("paged_decode_attn_bf16_window", (k_cache, v_cache), (),
-               _pools(k_cache, v_cache, torch.bfloat16), q, page_table, seq_lens, sm_scale,
-               (int(window), int(sinks)), out, lse, workspace, abort, num_ctas, stream)
+    shape = _need(k_cache, torch.bfloat16, 4, "k_cache").shape
+    _attn_call("paged_decode_attn_bf16_window", (k_cache, v_cache), (), shape,
+               _pool_specs(shape, torch.bfloat16, k_cache, v_cache), q, page_table, seq_lens,
+               sm_scale, (int(window), int(sinks)), out, lse, workspace, abort, num_ctas, stream)
 
 
 def paged_decode_attn_int4_window(q, k_codes, k_params, v_codes, v_params, page_table, seq_lens,
@@ -701,7 +714,8 @@ def paged_decode_attn_int4_window(q, k_codes, k_params, v_codes, v_params, page_
                                   num_ctas=0, stream=None):
     """paged_decode_attn_int4 over the last `window` and the first `sinks` tokens."""
     pools = (k_codes, k_params, v_codes, v_params)
-    _attn_call("paged_decode_attn_int4_window", pools, (), _int4_pools(*pools), q,
+    shape = _int4_shape(k_codes)
+    _attn_call("paged_decode_attn_int4_window", pools, (), shape, _int4_specs(shape, *pools), q,
                page_table, seq_lens, sm_scale, (int(window), int(sinks)), out, lse, workspace,
                abort, num_ctas, stream)
 
