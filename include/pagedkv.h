@@ -56,8 +56,10 @@
  *    waits for that kernel to finish before it touches memory that kernel
  *    may write, with one exception documented at paged_decode_attn_fp8:
  *    before waiting, attention reads q, seq_lens and page_table and
- *    prefetches K/V pages into L2 (nothing it reads before the wait reaches
- *    its outputs).
+ *    prefetches K/V pages into L2 (no K/V value it reads before the wait
+ *    reaches its outputs; q, seq_lens and page_table are inputs that no kernel
+ *    of the library writes, but for kv_extend_tables, which lets no kernel
+ *    behind it start before it has finished).
  *  - Errors: a status code is returned.  Invalid arguments are detected on
  *    the host before anything is enqueued (PKV_ERR_INVALID_ARG,
  *    PKV_ERR_WORKSPACE, PKV_ERR_UNSUPPORTED); a failed launch returns
