@@ -257,6 +257,69 @@ int64_t max_visible(int32_t max_pages, int32_t page_size, int32_t window, int32_
     return window > 0 ? std::min<int64_t>(all, static_cast<int64_t>(window) + sinks) : all;
 }
 
+// Whether the library's work split of a call comes from model_split (INT4 caches
+// and windows) or from plan_attention's rule on the item count (FP8 and BF16
+// without a window).
+bool modelled_split(int kv, int32_t window) { return kv == PKV_KV_INT4 || window > 0; }
+
+// Work split from an estimate of the slowest CTA's time, in us, at the longest
+// requests that the page table allows: a chunk costs more the more CTAs share an
+// SM, a segment (an item's part in a CTA: its prologue and epilogue) about as much
+// as two chunks, clusters of several CTAs their two barriers, split-K its merge
+// launch.  Constants from a B200: one chunk of a lone CTA 0.9 (INT4, two heads of
+// 128), 0.77 (FP8 two heads, BF16 one); 1.7 at three and 1.4 at two CTAs per SM;
+// items of one head 0.65 of two, heads of 64 dims 0.65 of 128; and no less than
+// 0.1 for each TMA box of a chunk, which one lane issues.
+// Measured, this choice / the item-count rule: INT4 64 x 8,192 tokens 135 / 147
+// (split-K), 2 x 131,072 81 / 160 (split-K), 128 x 16 15.4 / 25.9 (clusters of
+// one), FP8 window of 400 over 128 x 600 34.6 / 41.5 (clusters of one).
+pkv_status model_split(int kv, int head_dim, int group, bool window, int page_size, int64_t items,
+                       int wide, int64_t chunks, int grid, int* kv_per_item, int* cluster, int* nclusters) {
+    const DeviceInfo* info = nullptr;
+    pkv_status st = device_info(&info);
+    if (st != PKV_OK) return st;
+    constexpr double kSegment = 3.0, kBarriers = 3.0, kMerge = 6.0;
+    auto chunk = [&](double ctas, int heads) {
+        const double shared = std::max(0.0, ctas / info->sms - 1.0);
+        const double t = kv == PKV_KV_INT4 ? 0.9 + 0.4 * shared : 0.77 + 0.63 * shared;
+        int boxes = 2 * (page_size < pkv::kChunkTokens ? pkv::kChunkTokens / page_size : 1);
+        if (kv == PKV_KV_BF16 && head_dim == 128) boxes *= 2;
+        if (kv == PKV_KV_INT4) boxes = page_size < pkv::kChunkTokens ? 0 : 2 * boxes;
+        if (heads == 2 && page_size != pkv::kChunkTokens) boxes *= 2;
+        return std::max(t * (heads < 2 && kv != PKV_KV_BF16 ? 0.65 : 1.0) *
+                            (head_dim == 64 ? 0.65 : 1.0),
+                        0.1 * boxes);
+    };
+    *kv_per_item = wide;
+    *cluster = *nclusters = 0;
+    const double n = static_cast<double>(items);
+    double best = n * chunks / grid * chunk(grid, wide) + (n / grid + 1.0) * kSegment + kMerge;
+    // (few two-head items may be taken one head at a time, which doubles them)
+    for (int heads = wide; heads >= 1; --heads) {
+        if (heads < wide && items * 4 > info->sms) break;
+        const int64_t parts = items * (wide / heads);
+        const pkv::AttnVariant v = variant_of(kv, head_dim, group, heads, window);
+        for (int c = 1; c <= pkv::kMaxCluster; ++c) {
+            int kmax = 0;
+            st = max_clusters(v, c, &kmax);
+            if (st != PKV_OK) return st;
+            if (kmax <= 0) continue;
+            const int64_t k = std::min<int64_t>(parts, kmax);
+            const int64_t most = (parts + k - 1) / k;   // items of the fullest cluster
+            const double per = static_cast<double>(most);
+            const double t = per * chunks / c * chunk(static_cast<double>(k) * c, heads) +
+                             (c == 1 ? per * kSegment : (per / c + 1.0) * kSegment + kBarriers);
+            if (t < best) {
+                best = t;
+                *kv_per_item = heads;
+                *cluster = c;
+                *nclusters = static_cast<int>((parts + most - 1) / most);
+            }
+        }
+    }
+    return PKV_OK;
+}
+
 pkv_status plan_attention(int kv, int32_t batch, int32_t num_kv_heads, int32_t group,
                           int32_t head_dim, int32_t max_pages, int32_t page_size, int32_t window,
                           int32_t sinks, int32_t num_ctas, AttnPlan* plan,
@@ -279,7 +342,11 @@ pkv_status plan_attention(int kv, int32_t batch, int32_t num_kv_heads, int32_t g
             pkv::kChunkTokens;
         const int64_t max_units =
             static_cast<int64_t>(batch) * (num_kv_heads / kv_per_item) * chunks_per_seq;
-        const int64_t cap = std::max<int64_t>(info->sms, (max_units + 7) / 8);
+        int64_t cap = std::max<int64_t>(info->sms, (max_units + 7) / 8);
+        // INT4 and windows: nor fewer CTAs than items (short requests; measured with
+        // 128 x 16 tokens, 512 items: 18.3 us on 444 CTAs, 25.9 on 148)
+        if (modelled_split(kv, window))
+            cap = std::max<int64_t>(cap, static_cast<int64_t>(batch) * (num_kv_heads / kv_per_item));
         if (cap < grid) grid = static_cast<int>(cap);
     } else {
         const DeviceInfo* info = nullptr;
@@ -300,7 +367,13 @@ pkv_status plan_attention(int kv, int32_t batch, int32_t num_kv_heads, int32_t g
     // so the workspace size does not depend on this).
     int64_t items = static_cast<int64_t>(batch) * (num_kv_heads / kv_per_item);
     int cluster = 0, nclusters = 0;
-    if (allow_cluster && (num_ctas < 0 || (num_ctas == 0 && items <= grid))) {
+    if (allow_cluster && num_ctas == 0 && modelled_split(kv, window)) {
+        st = model_split(kv, head_dim, group, window > 0, page_size, items, kv_per_item,
+                         (max_visible(max_pages, page_size, window, sinks) + pkv::kChunkTokens - 1) /
+                             pkv::kChunkTokens,
+                         grid, &kv_per_item, &cluster, &nclusters);
+        if (st != PKV_OK) return st;
+    } else if (allow_cluster && (num_ctas < 0 || (num_ctas == 0 && items <= grid))) {
         if (num_ctas == 0 && kv_per_item == 2) {
             const DeviceInfo* info = nullptr;
             st = device_info(&info);
@@ -316,25 +389,6 @@ pkv_status plan_attention(int kv, int32_t batch, int32_t num_kv_heads, int32_t g
         if (cluster == 0 && num_ctas < 0)
             return fail(PKV_ERR_UNSUPPORTED, "clusters of %d CTAs do not fit on this device",
                         -num_ctas);
-        // INT4: split-K uses every resident CTA and costs a merge launch, about the
-        // time of two or three chunks of a CTA.  It is taken where the longest
-        // requests that the page table allows leave a CTA that many fewer (measured,
-        // cluster / split-K, 8 KV heads of 128 dims: 1 x 32,768 tokens 42 / 27 us, 4 x
-        // 8,192 28 / 28, 8 x 2,048 20 / 23, 8 x 32,768 132 / 81, 16 x 8,192 48 / 50,
-        // 64 x 8,192 147 / 135).
-        if (num_ctas == 0 && kv == PKV_KV_INT4 && cluster > 0) {
-            const int64_t chunks = (max_visible(max_pages, page_size, window, sinks) +
-                                    pkv::kChunkTokens - 1) / pkv::kChunkTokens;
-            const int wide = plan->ws_kv_per_item;
-            const double in_cluster = static_cast<double>((items + nclusters - 1) / nclusters) *
-                                      chunks / cluster * kv_per_item / wide;
-            const double in_split =
-                static_cast<double>(batch) * (num_kv_heads / wide) * chunks / grid;
-            if (in_cluster - in_split > 2.5) {
-                cluster = nclusters = 0;
-                kv_per_item = wide;
-            }
-        }
     }
     plan->kv_per_item = kv_per_item;
     plan->cluster = cluster;
