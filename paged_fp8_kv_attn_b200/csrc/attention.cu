@@ -572,7 +572,8 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
     walk.init(u_lo < u_hi ? scratch[8] : 0, u_lo < u_hi ? scratch[9] : 0, u_lo, u_hi);
 
 
-    const int P = a.page_size;
+    const int P = a.page_size;              // a power of two
+    const int pshift = 31 - __clz(P);
     const int box_rows = a.box_rows;
     // With two KV heads per item and 64-token pages (INT4: up to 64), the
     // item's K (or V) rows of a page are one contiguous box; otherwise one box
@@ -608,18 +609,18 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             int count = 0;
             while (count < S && w2.next(s)) {
                 win.reset(a.page_table + static_cast<int64_t>(s.b) * a.max_pages);
-                const int npages = (s.L + P - 1) / P;
+                const int npages = (s.L + P - 1) >> pshift;
                 for (int ch = s.c0; ch < s.c1 && count < S; ++ch, ++count) {
                     const int rc = s.real(ch);
                     for (int i = 0; i < boxes; ++i) {
                         const int tok0 = rc * kChunkTokens + i * box_toks;
-                        const int j = tok0 / P;
+                        const int j = tok0 >> pshift;
                         if (j >= npages) break;
                         if (hidden_box(s.L, tok0)) continue;
                         const int32_t pid = win.get(j, npages, lane);
                         if (lane == 0 && pid >= 0 && pid < a.num_pages) {
                             for (int kv = 0; kv < (joint ? 1 : kH); ++kv) {
-                                const int32_t y = (pid * Hkv + s.h * kH + kv) * P + (tok0 % P);
+                                const int32_t y = (pid * Hkv + s.h * kH + kv) * P + (tok0 & (P - 1));
                                 for (int st = 0; st < C::kSubTiles; ++st) {
                                     tma_prefetch_l2_2d(&tmap_k, st * 64, y);
                                     tma_prefetch_l2_2d(&tmap_v, st * 64, y);
@@ -642,10 +643,10 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // the L2 prefetch above already loaded for this row is kept)
         auto load_meta = [&](const Segment& sg, PageWindow& w) {
             const int32_t* row = a.page_table + static_cast<int64_t>(sg.b) * a.max_pages;
-            const int j0 = sg.real(sg.c0) * kChunkTokens / P;
+            const int j0 = sg.real(sg.c0) * kChunkTokens >> pshift;
             if (w.row != row || w.base != j0) {
                 w.reset(row);
-                w.preload(j0, (sg.L + P - 1) / P, lane);
+                w.preload(j0, (sg.L + P - 1) >> pshift, lane);
             }
             return (a.abort != nullptr) ? static_cast<int>(a.abort[sg.b]) : 0;
         };
@@ -657,7 +658,6 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             constexpr int kSteps = C::kTileBytes / 512;
             constexpr int kParPieces = C::kParTileBytes / 16;
             const uint32_t lane_off = swz<C::kRowBytes, C::kSwizzle>(0, lane * 16);
-            const int pshift = 31 - __clz(P);
             const int steps_shift = 31 - __clz(box_rows * C::kRowBytes / 512);   // steps of a box
             const int rows_shift = 31 - __clz(box_rows);
             const int32_t* row = w.row;
@@ -745,7 +745,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                     static_cast<int64_t>(s.h) * kH * a.group) * kD;
                 if (lane * 64 < kH * a.group * kD) prefetch_l2(a.q + q0 + lane * 64);
             }
-            const int npages = (s.L + P - 1) / P;
+            const int npages = (s.L + P - 1) >> pshift;
             if constexpr (kInt4) {
                 if (direct) copy_segment(s, win, npages, it);
             }
@@ -766,7 +766,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     pids[i] = -1;
                     if (i < boxes) {
                         const int tok0 = rc * kChunkTokens + i * box_toks;
-                        const int j = tok0 / P;
+                        const int j = tok0 >> pshift;
                         if (j < npages && !hidden_box(s.L, tok0)) {
                             pids[i] = win.get(j, npages, lane);
                             if (pids[i] < 0 || pids[i] >= a.num_pages) {
@@ -787,7 +787,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         if (pids[i] < 0) continue;
                         const int tok0 = rc * kChunkTokens + i * box_toks;
                         for (int kv = 0; kv < (joint ? 1 : kH); ++kv) {
-                            const int32_t y = (pids[i] * Hkv + s.h * kH + kv) * P + (tok0 % P);
+                            const int32_t y = (pids[i] * Hkv + s.h * kH + kv) * P + (tok0 & (P - 1));
                             for (int st = 0; st < C::kSubTiles; ++st) {
                                 const uint32_t off = kv * C::kHeadTileBytes + st * C::kSubTileBytes +
                                                      i * box_rows * C::kBoxBytes;
