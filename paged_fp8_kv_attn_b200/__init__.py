@@ -404,7 +404,8 @@ def _append_specs(k_new, v_new, page_table, seq_lens, page_size, shape, B, MP):
     _, Hkv, P, D = shape
     if page_size != P:
         raise ValueError(f"page_size is {page_size}, the cache's pages hold {P} tokens")
-    return (("k_new", k_new, torch.bfloat16, (B, Hkv, D)), ("v_new", v_new, torch.bfloat16, (B, Hkv, D)),
+    new = (B, Hkv, D)
+    return (("k_new", k_new, torch.bfloat16, new), ("v_new", v_new, torch.bfloat16, new),
             ("page_table", page_table, torch.int32, (B, MP)), ("seq_lens", seq_lens, torch.int32, (B,)))
 
 

@@ -269,26 +269,34 @@ bool modelled_split(int kv, int32_t window) { return kv == PKV_KV_INT4 || window
 // launch.  Constants from a B200: one chunk of a lone CTA 0.9 (INT4, two heads of
 // 128), 0.77 (FP8 two heads, BF16 one); 1.7 at three and 1.4 at two CTAs per SM;
 // items of one head 0.65 of two, heads of 64 dims 0.65 of 128; and no less than
-// 0.1 for each TMA box of a chunk, which one lane issues.
+// 0.07 for each TMA box of a chunk, which one lane issues.
+// Requests of one batch differ in length, which split-K evens out and whole items
+// do not: a cluster's chunks count 25% more, but for a window shorter than the
+// table's longest request, which makes most of them equal (96 requests of up to
+// 8,190 tokens, 64 dims: clusters of one 116, split-K 77).
 // Measured, this choice / the item-count rule: INT4 64 x 8,192 tokens 135 / 147
 // (split-K), 2 x 131,072 81 / 160 (split-K), 128 x 16 15.4 / 25.9 (clusters of
 // one), FP8 window of 400 over 128 x 600 34.6 / 41.5 (clusters of one).
-pkv_status model_split(int kv, int head_dim, int group, bool window, int page_size, int64_t items,
-                       int wide, int64_t chunks, int grid, int* kv_per_item, int* cluster, int* nclusters) {
+pkv_status model_split(int kv, int head_dim, int group, bool window, int page_size, int32_t batch,
+                       int64_t items, int wide, int64_t chunks, int grid, int* kv_per_item,
+                       int* cluster, int* nclusters) {
     const DeviceInfo* info = nullptr;
     pkv_status st = device_info(&info);
     if (st != PKV_OK) return st;
     constexpr double kSegment = 3.0, kBarriers = 3.0, kMerge = 6.0;
+    const double uneven = window ? 1.0 : 1.0 + 0.25 * (1.0 - 1.0 / batch);
     auto chunk = [&](double ctas, int heads) {
         const double shared = std::max(0.0, ctas / info->sms - 1.0);
         const double t = kv == PKV_KV_INT4 ? 0.9 + 0.4 * shared : 0.77 + 0.63 * shared;
-        int boxes = 2 * (page_size < pkv::kChunkTokens ? pkv::kChunkTokens / page_size : 1);
+        int boxes = 2 * std::max(1, pkv::kChunkTokens / page_size);
         if (kv == PKV_KV_BF16 && head_dim == 128) boxes *= 2;
-        if (kv == PKV_KV_INT4) boxes = page_size < pkv::kChunkTokens ? 0 : 2 * boxes;
-        if (heads == 2 && page_size != pkv::kChunkTokens) boxes *= 2;
+        if (kv == PKV_KV_INT4) boxes = page_size <= pkv::int4_direct_page(head_dim) ? 0 : 2 * boxes;
+        const bool joint = kv == PKV_KV_INT4 ? page_size <= pkv::kChunkTokens
+                                             : page_size == pkv::kChunkTokens;
+        if (heads == 2 && !joint) boxes *= 2;
         return std::max(t * (heads < 2 && kv != PKV_KV_BF16 ? 0.65 : 1.0) *
                             (head_dim == 64 ? 0.65 : 1.0),
-                        0.1 * boxes);
+                        0.07 * boxes);
     };
     *kv_per_item = wide;
     *cluster = *nclusters = 0;
@@ -307,7 +315,7 @@ pkv_status model_split(int kv, int head_dim, int group, bool window, int page_si
             const int64_t k = std::min<int64_t>(parts, kmax);
             const int64_t most = (parts + k - 1) / k;   // items of the fullest cluster
             const double per = static_cast<double>(most);
-            const double t = per * chunks / c * chunk(static_cast<double>(k) * c, heads) +
+            const double t = uneven * per * chunks / c * chunk(static_cast<double>(k) * c, heads) +
                              (c == 1 ? per * kSegment : (per / c + 1.0) * kSegment + kBarriers);
             if (t < best) {
                 best = t;
@@ -368,7 +376,7 @@ pkv_status plan_attention(int kv, int32_t batch, int32_t num_kv_heads, int32_t g
     int64_t items = static_cast<int64_t>(batch) * (num_kv_heads / kv_per_item);
     int cluster = 0, nclusters = 0;
     if (allow_cluster && num_ctas == 0 && modelled_split(kv, window)) {
-        st = model_split(kv, head_dim, group, window > 0, page_size, items, kv_per_item,
+        st = model_split(kv, head_dim, group, window > 0, page_size, batch, items, kv_per_item,
                          (max_visible(max_pages, page_size, window, sinks) + pkv::kChunkTokens - 1) /
                              pkv::kChunkTokens,
                          grid, &kv_per_item, &cluster, &nclusters);
@@ -1061,7 +1069,7 @@ pkv_status kv_extend_tables(const int32_t* old_lens, const int32_t* new_lens, in
     if (free_capacity > num_pages)
         return fail(PKV_ERR_INVALID_ARG, "free_capacity must be at most num_pages");
     if ((page_tags == nullptr) != (expected_tags == nullptr))
-        return fail(PKV_ERR_INVALID_ARG, "page_tags and expected_tags are given together or not at all");
+        return fail(PKV_ERR_INVALID_ARG, "page_tags and expected_tags are given together or neither is");
     if (!num_free || !num_free_out || !cu_tokens || (free_capacity > 0 && !free_pages) ||
         (max_tokens > 0 && !slot_map) ||
         (batch > 0 && (!old_lens || !new_lens || !page_table || !failed)))
@@ -1215,9 +1223,9 @@ size_t paged_decode_attn_workspace_size(int32_t kv_dtype, int32_t batch, int32_t
     if (grid == 0) {
         // the larger of the grids without and with a window: one workspace serves both calls
         for (const bool window : {false, true}) {
+            const auto v = variant_of(kv_dtype, head_dim, group, kv_per_item, window);
             int ctas = 0;
-            if (default_ctas(variant_of(kv_dtype, head_dim, group, kv_per_item, window), &ctas) != PKV_OK)
-                return 0;
+            if (default_ctas(v, &ctas) != PKV_OK) return 0;
             grid = std::max(grid, ctas);
         }
     }

@@ -1,5 +1,6 @@
-// attention.cu -- paged decode attention over an FP8 E4M3 or BF16 KV cache
-// for sm_100a: split-K partial kernel plus log-sum-exp merge kernel.
+// attention.cu -- paged decode attention over an FP8 E4M3, BF16 or INT4 KV
+// cache, with or without a sliding window, for sm_100a: split-K partial kernel
+// plus log-sum-exp merge kernel.
 //
 // Source pages: "大模型推理优化：量化、压缩与安全验证", section "量化 KV cache"
 // (FP8 e4m3 cache; the FP8 attention kernel converts values on every read);
@@ -39,6 +40,14 @@
 //  * Lazy rescaling: a warp rescales O only when a head's running maximum
 //    grows by more than 8 (log2 units); P is then at most 2^8, exact enough
 //    in f16 and far from overflow.
+//  * INT4: a value is s code + m per token and group of 64 dims, so
+//    q . k = sum_groups s (q . code) + m sum(q), and the weighted sum of V is
+//    sum (w s) code + sum w m.  The products run over the codes as they lie in
+//    shared memory (one AND makes an operand pair); scales and minima are applied
+//    per token.  Bound by issue and the ALU pipe, not by memory: 64 x 8,192 tokens
+//    of 8 heads x 128 dims take 133 us where their 606 MB take 92.
+//  * Window: units are the chunks that hold a visible token; the ones at its
+//    edges mask scores and V rows as the last chunk of a request does.
 #include "device.cuh"
 #include "internal.h"
 
@@ -69,11 +78,11 @@ struct AttnCfg {
     static constexpr int kParTileBytes = kH * kChunkTokens * kParRowBytes;
     // INT4 pages of at most this many tokens are copied 16 bytes a lane by the
     // whole producer warp; larger ones as TMA boxes.  A box costs its one issuing
-    // lane the same whatever its size, so it pays from 8 KB of codes on.  Measured
-    // (444 CTAs, TMA / copies): D = 128, 64 x 8,192 tokens, pages of 64: 135 / 149 us,
-    // of 32: 179 / 148, of 16: 242 / 149; D = 64, 96 ragged requests, pages of 64:
-    // 79 / 73, of 32: 110 / 73, of 16: 163 / 77.
-    static constexpr int kDirectPage = kInt4 ? (kD == 128 ? 32 : 64) : 0;
+    // lane the same whatever its size, so it pays from 4 KB of codes on.  Measured
+    // (444 CTAs, TMA / copies): D = 128, 64 x 8,192 tokens, pages of 64: 133 / 149 us,
+    // of 32: 138 / 153, of 16: 169 / 155; D = 64, 96 ragged requests, pages of 64:
+    // 73 / 75, of 32: 83 / 75, of 16: 112 / 77.
+    static constexpr int kDirectPage = kInt4 ? int4_direct_page(kD) : 0;
     static constexpr int kStageBytes = (2 * (kTileBytes + kParTileBytes) + 1023) / 1024 * 1024;
     // Pipeline depth and resident CTAs per SM, chosen by measurement on B200:
     // resident warps matter more than depth (each CTA keeps up to kStages
@@ -684,7 +693,8 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const int32_t y = (pid * Hkv + sg.h * kH) << pshift;   // first pool row
                 if (iter >= static_cast<uint32_t>(S)) {
                     if (lane == 0)
-                        wait_or_give_up(&empty_bar[stage], ((iter / S) + 1) & 1, cta_failed, a.ws_status);
+                        wait_or_give_up(&empty_bar[stage], ((iter / S) + 1) & 1, cta_failed,
+                                        a.ws_status);
                     __syncwarp();
                 }
                 const uint32_t kdst = smem_addr(smem + stage * C::kStageBytes);
@@ -695,8 +705,9 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
                 for (int st = 0; st < kSteps; ++st) {
                     const int b = st >> steps_shift;
-                    const int64_t src = static_cast<int64_t>(__shfl_sync(0xffffffffu, y, b)) * C::kRowBytes +
-                                        (st - (b << steps_shift)) * 512 + lane * 16;
+                    const int64_t row0 = __shfl_sync(0xffffffffu, y, b);
+                    const int64_t src =
+                        row0 * C::kRowBytes + (st - (b << steps_shift)) * 512 + lane * 16;
                     if ((use >> b) & 1) {
                         const uint32_t dst = kdst + st * 512 + lane_off;
                         cp_async16(dst, a.k_codes + src);
@@ -837,16 +848,15 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
     constexpr int kMB = kD / 16;      // m-blocks of the head dimension (PV)
     constexpr int kKS = kD / 16;      // k-steps of the QK contraction
 
-    // INT4: the first row, in a K or V tile of the item, of the warp's 16-token
-    // tile t (rows run token by token inside a page, then over the item's KV heads)
-    auto tile_row = [&](int t) {
-        const int rb = row0 + 16 * t;
-        if constexpr (kH == 1) return rb;
-        return (rb / box_toks * 2 + kvh_w) * box_toks + rb % box_toks;
-    };
+    // INT4: the first row, in a K or V tile of the item, of the warp's tile t of
+    // 16 tokens (joint boxes: rows run over a page's tokens, then over the heads)
     uint32_t trow[kH];
 #pragma unroll
-    for (int t = 0; t < kH; ++t) trow[t] = kInt4 ? (joint ? tile_row(t) : kvh_w * kChunkTokens + row0 + 16 * t) : 0;
+    for (int t = 0; t < kH; ++t) {
+        const int rb = row0 + 16 * t;
+        trow[t] = joint ? (rb / box_toks * 2 + kvh_w) * box_toks + rb % box_toks
+                        : kvh_w * kChunkTokens + rb;
+    }
     // Fixed shared-memory offsets of this thread's K and V reads.
     uint32_t k_off[2][kD / 64];       // FP8: rows tau(g), 8+tau(g); chunks c, 4+c
     uint32_t v_off[4];                // FP8: rows tau(2c), tau(2c+1), 8+.., 8+..; chunk g
@@ -865,10 +875,11 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             v_off[i] = swz<C::kRowBytes, C::kSwizzle>(vr[i], (kD == 128 ? 16 : 8) * g);
     }
     // INT4: the row in a 16-row tile and the 16-byte column of this lane's
-    // ldmatrix addresses, per group of 64 dims (16 rows on, the swizzle repeats).  K (matrices: rows 0-7 and 8-15 of the group's first
-    // half, then of its second): a lane gets the 8 dims 8c.. of row g, g + 8,
-    // then the dims 32 + 8c...  V (transposed; token rows 0-7 of both halves,
-    // then 8-15): a lane gets dims 4g.. of tokens 2c and 2c + 1 in one word.
+    // ldmatrix addresses, per group of 64 dims (16 rows on, the swizzle repeats).
+    // K (matrices: rows 0-7 and 8-15 of the group's first half, then of its
+    // second): a lane gets the 8 dims 8c.. of row g, g + 8, then the dims
+    // 32 + 8c...  V (transposed; token rows 0-7 of both halves, then 8-15): a lane
+    // gets dims 4g.. of tokens 2c and 2c + 1 in one word.
     uint32_t k4_off[C::kGroups], v4_off[C::kGroups];
     if constexpr (kInt4) {
         const int r8 = lane & 7, m = lane >> 3;
@@ -1058,7 +1069,10 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         qy[nb][0] = c < 2 ? p0 : p1;
                         qy[nb][1] = c < 2 ? p2 : 0u;
                     } else {
-                        qy[nb][0] = c == 0 ? parts[0][0] : (c == 1 ? parts[0][1] : (c == 2 ? parts[0][2] : 0u));
+                        qy[nb][0] = c == 0   ? parts[0][0]
+                                    : c == 1 ? parts[0][1]
+                                    : c == 2 ? parts[0][2]
+                                             : 0u;
                         qy[nb][1] = 0u;
                     }
                     // (the codes read as code * 2^-24)

@@ -136,6 +136,9 @@ struct WorkspaceLayout {
 WorkspaceLayout workspace_layout(int32_t batch, int32_t group, int32_t num_kv_heads,
                                  int32_t kv_per_item, int32_t head_dim, int32_t num_ctas);
 
+// INT4 attention: largest page that the producer warp copies itself.
+constexpr int int4_direct_page(int head_dim) { return head_dim == 128 ? 16 : 32; }
+
 // One compiled variant of the attention kernel.
 struct AttnVariant {
     int kv;            // kKvFp8, kKvBf16 or kKvInt4

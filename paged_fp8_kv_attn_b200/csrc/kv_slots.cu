@@ -155,14 +155,14 @@ static cudaError_t launch_slots(K kernel, const SlotArgs& a, cudaStream_t stream
 
 cudaError_t launch_write_slots(const KvDst& dst, const uint16_t* k_new, const uint16_t* v_new,
                                const SlotArgs& a, cudaStream_t stream) {
-    return launch_slots(PKV_SLOT_KERNEL(write_slots_kernel, dst.kv, a.head_dim, slot_tokens(a) == 1), a, stream, dst,
-                        k_new, v_new);
+    auto* kernel = PKV_SLOT_KERNEL(write_slots_kernel, dst.kv, a.head_dim, slot_tokens(a) == 1);
+    return launch_slots(kernel, a, stream, dst, k_new, v_new);
 }
 
 cudaError_t launch_read_slots(const KvDst& src, uint16_t* k_out, uint16_t* v_out,
                               const SlotArgs& a, cudaStream_t stream) {
-    return launch_slots(PKV_SLOT_KERNEL(read_slots_kernel, src.kv, a.head_dim, slot_tokens(a) == 1), a, stream, src,
-                        k_out, v_out);
+    auto* kernel = PKV_SLOT_KERNEL(read_slots_kernel, src.kv, a.head_dim, slot_tokens(a) == 1);
+    return launch_slots(kernel, a, stream, src, k_out, v_out);
 }
 
 }  // namespace pkv

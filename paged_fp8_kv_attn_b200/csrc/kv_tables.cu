@@ -59,7 +59,9 @@ __global__ void __launch_bounds__(kTableThreads) extend_tables_kernel(const Tabl
     const bool wide = reinterpret_cast<uintptr_t>(a.slot_map) % 16 == 0;
     auto pages_of = [&](int32_t len) { return (static_cast<uint32_t>(len) + P - 1) >> shift; };
     // the free stack's entry for the i-th page of the call
-    auto stack_entry = [&](uint32_t i) { return a.free_pages + (num_free - 1 - static_cast<int32_t>(i)); };
+    auto stack_entry = [&](uint32_t i) {
+        return a.free_pages + (num_free - 1 - static_cast<int32_t>(i));
+    };
 
     uint32_t pages0 = 0, toks0 = 0;   // before the pass's first row
     uint32_t taken = 0;               // pages of the rows served so far

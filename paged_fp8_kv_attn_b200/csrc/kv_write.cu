@@ -1,5 +1,5 @@
-// kv_write.cu -- the batched page-tag check, the FP8 / BF16 append of the
-// new token, and the BF16 -> FP8 page handoff.
+// kv_write.cu -- the batched page-tag check, the FP8 / BF16 / INT4 append of
+// the new token, and the BF16 -> FP8 and BF16 -> INT4 page handoffs.
 //
 // Source pages: "大模型推理优化：量化、压缩与安全验证", sections "量化 KV cache"
 // (FP8 e4m3 cache) and "保护共享 KV cache" (per-page tags, per-request
@@ -288,7 +288,8 @@ cudaError_t launch_expected_tags(const uint32_t* page_tags, int32_t num_pages,
 }
 
 // ---------------------------------------------------------------------------
-// BF16 -> FP8 page handoff: grid-stride over 16-element groups
+// BF16 -> FP8 (INT4) page handoff: grid-stride over 16-element groups (8-element
+// blocks)
 // ---------------------------------------------------------------------------
 constexpr int kRequantThreads = 256;
 
