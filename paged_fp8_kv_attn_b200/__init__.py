@@ -186,8 +186,12 @@ def _on(stream):
     return stream.device_index, stream.cuda_stream
 
 
-def _args(dev, *specs):
-    """Each (name, tensor, dtype, shape): contiguous, on the call's device."""
+def _args(dev, anchors, *specs):
+    """Each (name, tensor, dtype, shape): contiguous, on the call's device; anchors, the
+    tensors that gave the shapes and are checked otherwise: on the call's device."""
+    for t in anchors:
+        if t.get_device() != dev:
+            raise ValueError(f"tensors must be on the call's device {dev}, got {t.device}")
     for name, t, dtype, shape in specs:
         if t is None or t.get_device() != dev or t.dtype is not dtype or t.shape != shape \
                 or not t.is_contiguous():
@@ -212,16 +216,12 @@ def _int4_shape(k_codes):
     return NP, Hkv, P, 2 * half
 
 
-def _int4_specs(shape, k_codes, k_params, v_codes, v_params):
+def _int4_specs(shape, k_params, v_codes, v_params):
+    """Of the tensors that go with the K codes."""
     NP, Hkv, P, D = shape
     codes, params = (NP, Hkv, P, D // 2), (NP, Hkv, P, D // INT4_GROUP, 2)
-    return (("k_codes", k_codes, torch.uint8, codes), ("k_params", k_params, torch.bfloat16, params),
-            ("v_codes", v_codes, torch.uint8, codes), ("v_params", v_params, torch.bfloat16, params))
-
-
-def _pool_specs(shape, dtype, k_cache, v_cache):
-    """Of an FP8 or BF16 cache."""
-    return ("k_cache", k_cache, dtype, shape), ("v_cache", v_cache, dtype, shape)
+    return (("k_params", k_params, torch.bfloat16, params), ("v_codes", v_codes, torch.uint8, codes),
+            ("v_params", v_params, torch.bfloat16, params))
 
 
 _TAG_DTYPES = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
@@ -251,11 +251,10 @@ def kv_tag_check_window(page_tags, page_table, expected_tags, seq_lens, page_siz
     B, MP = _need(page_table, i32, 2, "page_table").shape
     tag = _tag_dtype(page_tags, "page_tags")
     dev, handle = _on(stream)
-    _args(dev, ("page_tags", page_tags, tag, page_tags.shape), ("page_table", page_table, i32, (B, MP)),
-          ("expected_tags", expected_tags, tag, (B, MP)), ("seq_lens", seq_lens, i32, (B,)),
+    _args(dev, (page_tags, page_table), ("expected_tags", expected_tags, tag, (B, MP)), ("seq_lens", seq_lens, i32, (B,)),
           ("abort_out", abort_out, torch.uint8, (B,)))
     if num_aborted is not None:
-        _args(dev, ("num_aborted", num_aborted, i32, (1,)))
+        _args(dev, (), ("num_aborted", num_aborted, i32, (1,)))
     _check("kv_tag_check_window", _load().kv_tag_check_window(
         _ptr(page_tags), page_tags.shape[0], _ptr(page_table), _ptr(expected_tags), MP,
         _ptr(seq_lens), B, page_size, int(window), int(sinks), _ptr(abort_out), _ptr(num_aborted),
@@ -370,10 +369,10 @@ def kv_append_int4(k_new, v_new, page_table, seq_lens, page_size, k_codes, k_par
     shape = NP, Hkv, P, D = _int4_shape(k_codes)
     B, MP = _need(page_table, torch.int32, 2, "page_table").shape
     dev, handle = _on(stream)
-    _args(dev, *_int4_specs(shape, k_codes, k_params, v_codes, v_params),
-          *_append_specs(k_new, v_new, page_table, seq_lens, page_size, shape, B, MP))
+    _args(dev, (k_codes, page_table), *_int4_specs(shape, k_params, v_codes, v_params),
+          *_append_specs(k_new, v_new, seq_lens, page_size, shape, B))
     if abort is not None:
-        _args(dev, ("abort", abort, torch.uint8, (B,)))
+        _args(dev, (), ("abort", abort, torch.uint8, (B,)))
     _check("kv_append_int4", _load().kv_append_int4(
         _ptr(k_new), _ptr(v_new), _ptr(page_table), MP, _ptr(seq_lens), B, Hkv, D, P,
         _ptr(k_codes), _ptr(k_params), _ptr(v_codes), _ptr(v_params), NP, _ptr(abort), handle))
@@ -387,26 +386,26 @@ def kv_check_append_int4(page_tags, page_table, expected_tags, seq_lens, page_si
     B, MP = _need(page_table, torch.int32, 2, "page_table").shape
     tag = _tag_dtype(page_tags, "page_tags")
     dev, handle = _on(stream)
-    _args(dev, *_int4_specs(shape, k_codes, k_params, v_codes, v_params),
-          *_append_specs(k_new, v_new, page_table, seq_lens, page_size, shape, B, MP),
+    _args(dev, (k_codes, page_table), *_int4_specs(shape, k_params, v_codes, v_params),
+          *_append_specs(k_new, v_new, seq_lens, page_size, shape, B),
           ("page_tags", page_tags, tag, (NP,)), ("expected_tags", expected_tags, tag, (B, MP)),
           ("abort_out", abort_out, torch.uint8, (B,)))
     if num_aborted is not None:
-        _args(dev, ("num_aborted", num_aborted, torch.int32, (1,)))
+        _args(dev, (), ("num_aborted", num_aborted, torch.int32, (1,)))
     _check("kv_check_append_int4", _load().kv_check_append_int4(
         _ptr(page_tags), NP, _ptr(page_table), _ptr(expected_tags), MP, _ptr(seq_lens), B, P,
         _ptr(k_new), _ptr(v_new), Hkv, D, _ptr(k_codes), _ptr(k_params), _ptr(v_codes),
         _ptr(v_params), _ptr(abort_out), _ptr(num_aborted), handle))
 
 
-def _append_specs(k_new, v_new, page_table, seq_lens, page_size, shape, B, MP):
+def _append_specs(k_new, v_new, seq_lens, page_size, shape, B):
     """Of an append to a cache of that shape."""
     _, Hkv, P, D = shape
     if page_size != P:
         raise ValueError(f"page_size is {page_size}, the cache's pages hold {P} tokens")
     new = (B, Hkv, D)
     return (("k_new", k_new, torch.bfloat16, new), ("v_new", v_new, torch.bfloat16, new),
-            ("page_table", page_table, torch.int32, (B, MP)), ("seq_lens", seq_lens, torch.int32, (B,)))
+            ("seq_lens", seq_lens, torch.int32, (B,)))
 
 
 def _token_rows(t, name, T, Hkv, D, dev):
@@ -429,7 +428,7 @@ def _slot_call(name, slot_map, pools, scales, k, v, shape, specs, write, stream)
     T = _need(slot_map, torch.int32, 1, "slot_map").numel()
     NP, Hkv, P, D = shape
     dev, handle = _on(stream)
-    _args(dev, *specs, ("slot_map", slot_map, torch.int32, (T,)))
+    _args(dev, (slot_map, pools[0]), *specs)
     ks, vs = _token_rows(k, "k", T, Hkv, D, dev), _token_rows(v, "v", T, Hkv, D, dev)
     rows = (k.data_ptr(), v.data_ptr(), ks, vs)
     cache = (slot_map.data_ptr(), T, Hkv, D, P, *scales, *[t.data_ptr() for t in pools], NP)
@@ -441,14 +440,14 @@ def kv_write_slots_fp8(k_new, v_new, slot_map, k_scale, v_scale, k_cache, v_cach
     """Quantise token rows to E4M3 and write row i into slot slot_map[i] (negative: skipped)."""
     shape = _need(k_cache, torch.uint8, 4, "k_cache").shape
     _slot_call("kv_write_slots_fp8", slot_map, (k_cache, v_cache), (float(k_scale), float(v_scale)),
-               k_new, v_new, shape, _pool_specs(shape, torch.uint8, k_cache, v_cache), True, stream)
+               k_new, v_new, shape, (("v_cache", v_cache, torch.uint8, shape),), True, stream)
 
 
 def kv_write_slots_bf16(k_new, v_new, slot_map, k_cache, v_cache, stream=None):
     """Write token row i into slot slot_map[i] of a BF16 cache (negative: skipped)."""
     shape = _need(k_cache, torch.bfloat16, 4, "k_cache").shape
     _slot_call("kv_write_slots_bf16", slot_map, (k_cache, v_cache), (), k_new, v_new, shape,
-               _pool_specs(shape, torch.bfloat16, k_cache, v_cache), True, stream)
+               (("v_cache", v_cache, torch.bfloat16, shape),), True, stream)
 
 
 def kv_write_slots_int4(k_new, v_new, slot_map, k_codes, k_params, v_codes, v_params, stream=None):
@@ -456,21 +455,21 @@ def kv_write_slots_int4(k_new, v_new, slot_map, k_codes, k_params, v_codes, v_pa
     pools = (k_codes, k_params, v_codes, v_params)
     shape = _int4_shape(k_codes)
     _slot_call("kv_write_slots_int4", slot_map, pools, (), k_new, v_new, shape,
-               _int4_specs(shape, *pools), True, stream)
+               _int4_specs(shape, *pools[1:]), True, stream)
 
 
 def kv_read_slots_fp8(slot_map, k_scale, v_scale, k_cache, v_cache, k_out, v_out, stream=None):
     """The bf16 values of the slots that slot_map names (zeros for none) of an E4M3 cache."""
     shape = _need(k_cache, torch.uint8, 4, "k_cache").shape
     _slot_call("kv_read_slots_fp8", slot_map, (k_cache, v_cache), (float(k_scale), float(v_scale)),
-               k_out, v_out, shape, _pool_specs(shape, torch.uint8, k_cache, v_cache), False, stream)
+               k_out, v_out, shape, (("v_cache", v_cache, torch.uint8, shape),), False, stream)
 
 
 def kv_read_slots_bf16(slot_map, k_cache, v_cache, k_out, v_out, stream=None):
     """The values of the slots that slot_map names (zeros for none) of a BF16 cache."""
     shape = _need(k_cache, torch.bfloat16, 4, "k_cache").shape
     _slot_call("kv_read_slots_bf16", slot_map, (k_cache, v_cache), (), k_out, v_out, shape,
-               _pool_specs(shape, torch.bfloat16, k_cache, v_cache), False, stream)
+               (("v_cache", v_cache, torch.bfloat16, shape),), False, stream)
 
 
 def kv_read_slots_int4(slot_map, k_codes, k_params, v_codes, v_params, k_out, v_out, stream=None):
@@ -478,7 +477,7 @@ def kv_read_slots_int4(slot_map, k_codes, k_params, v_codes, v_params, k_out, v_
     pools = (k_codes, k_params, v_codes, v_params)
     shape = _int4_shape(k_codes)
     _slot_call("kv_read_slots_int4", slot_map, pools, (), k_out, v_out, shape,
-               _int4_specs(shape, *pools), False, stream)
+               _int4_specs(shape, *pools[1:]), False, stream)
 
 
 def kv_extend_tables(old_lens, new_lens, page_size, free_pages, num_free, page_table, slot_map,
@@ -493,16 +492,15 @@ def kv_extend_tables(old_lens, new_lens, page_size, free_pages, num_free, page_t
     T = _need(slot_map, i32, 1, "slot_map").numel()
     cap = _need(free_pages, i32, 1, "free_pages").numel()
     dev, handle = _on(stream)
-    _args(dev, ("old_lens", old_lens, i32, (B,)), ("new_lens", new_lens, i32, (B,)),
-          ("free_pages", free_pages, i32, (cap,)), ("num_free", num_free, i32, (1,)),
-          ("num_free_out", num_free_out, i32, (1,)), ("page_table", page_table, i32, (B, MP)),
-          ("slot_map", slot_map, i32, (T,)), ("cu_tokens", cu_tokens, i32, (B + 1,)),
+    _args(dev, (page_table, slot_map, free_pages), ("old_lens", old_lens, i32, (B,)),
+          ("new_lens", new_lens, i32, (B,)), ("num_free", num_free, i32, (1,)),
+          ("num_free_out", num_free_out, i32, (1,)), ("cu_tokens", cu_tokens, i32, (B + 1,)),
           ("failed", failed, torch.uint8, (B,)))
     if page_tags is not None or expected_tags is not None:
         if page_tags is None or expected_tags is None:
             raise ValueError("page_tags and expected_tags are given together or not at all")
         tag = _tag_dtype(page_tags, "page_tags")
-        _args(dev, ("page_tags", page_tags, tag, (num_pages,)),
+        _args(dev, (), ("page_tags", page_tags, tag, (num_pages,)),
               ("expected_tags", expected_tags, tag, (B, MP)))
     _check("kv_extend_tables", _load().kv_extend_tables(
         old_lens.data_ptr(), new_lens.data_ptr(), B, int(page_size), free_pages.data_ptr(), cap,
@@ -533,8 +531,7 @@ def kv_requant_pages_int4(src_pool, src_pages, dst_codes, dst_params, dst_pages,
     N = _need(src_pages, torch.int32, 1, "src_pages").numel()
     NPd = _need(dst_codes, torch.uint8, 4, "dst_codes").shape[0]
     dev, handle = _on(stream)
-    _args(dev, ("src_pool", src_pool, torch.bfloat16, (NPs, Hkv, P, D)),
-          ("src_pages", src_pages, torch.int32, (N,)), ("dst_pages", dst_pages, torch.int32, (N,)),
+    _args(dev, (src_pool, src_pages), ("dst_pages", dst_pages, torch.int32, (N,)),
           ("dst_codes", dst_codes, torch.uint8, (NPd, Hkv, P, D // 2)),
           ("dst_params", dst_params, torch.bfloat16, (NPd, Hkv, P, D // INT4_GROUP, 2)))
     _check("kv_requant_pages_int4", _load().kv_requant_pages_int4(
@@ -667,15 +664,15 @@ def _attn_call(name, pools, scales, shape, specs, q, page_table, seq_lens, sm_sc
     B, Hq, Dq = _need(q, torch.bfloat16, 3, "q").shape
     if Dq != D:
         raise ValueError("head_dim of q and cache differ")
-    MP = _need(page_table, torch.int32, 2, "page_table").shape[1]
+    rows, MP = _need(page_table, torch.int32, 2, "page_table").shape
     ws = _need(workspace, torch.uint8, 1, "workspace").numel()
     dev, handle = _on(stream)
-    _args(dev, *specs, ("q", q, torch.bfloat16, (B, Hq, D)),
-          ("page_table", page_table, torch.int32, (B, MP)), ("seq_lens", seq_lens, torch.int32, (B,)),
-          ("out", out, torch.bfloat16, (B, Hq, D)), ("lse", lse, torch.float32, (B, Hq)),
-          ("workspace", workspace, torch.uint8, (ws,)))
+    if rows != B:
+        raise ValueError(f"page_table must have a row for each of {B} requests")
+    _args(dev, (q, pools[0], page_table, workspace), *specs, ("seq_lens", seq_lens, torch.int32, (B,)),
+          ("out", out, torch.bfloat16, (B, Hq, D)), ("lse", lse, torch.float32, (B, Hq)))
     if abort is not None:
-        _args(dev, ("abort", abort, torch.uint8, (B,)))
+        _args(dev, (), ("abort", abort, torch.uint8, (B,)))
     _check(name, getattr(_load(), name)(
         q.data_ptr(), *[t.data_ptr() for t in pools], *scales, page_table.data_ptr(), MP,
         seq_lens.data_ptr(), B, Hq, Hkv, D, P, NP, float(sm_scale), *window, _ptr(abort),
@@ -687,7 +684,7 @@ def paged_decode_attn_int4(q, k_codes, k_params, v_codes, v_params, page_table, 
     """Decode attention over a paged INT4 cache; writes out (bf16) and lse (fp32)."""
     pools = (k_codes, k_params, v_codes, v_params)
     shape = _int4_shape(k_codes)
-    _attn_call("paged_decode_attn_int4", pools, (), shape, _int4_specs(shape, *pools), q, page_table,
+    _attn_call("paged_decode_attn_int4", pools, (), shape, _int4_specs(shape, *pools[1:]), q, page_table,
                seq_lens, sm_scale, (), out, lse, workspace, abort, num_ctas, stream)
 
 
@@ -697,7 +694,7 @@ def paged_decode_attn_fp8_window(q, k_cache, v_cache, k_scale, v_scale, page_tab
     """paged_decode_attn_fp8 over the last `window` and the first `sinks` tokens."""
     shape = _need(k_cache, torch.uint8, 4, "k_cache").shape
     _attn_call("paged_decode_attn_fp8_window", (k_cache, v_cache), (float(k_scale), float(v_scale)),
-               shape, _pool_specs(shape, torch.uint8, k_cache, v_cache), q, page_table, seq_lens,
+               shape, (("v_cache", v_cache, torch.uint8, shape),), q, page_table, seq_lens,
                sm_scale, (int(window), int(sinks)), out, lse, workspace, abort, num_ctas, stream)
 
 
@@ -706,7 +703,7 @@ def paged_decode_attn_bf16_window(q, k_cache, v_cache, page_table, seq_lens, sm_
     """paged_decode_attn_bf16 over the last `window` and the first `sinks` tokens."""
     shape = _need(k_cache, torch.bfloat16, 4, "k_cache").shape
     _attn_call("paged_decode_attn_bf16_window", (k_cache, v_cache), (), shape,
-               _pool_specs(shape, torch.bfloat16, k_cache, v_cache), q, page_table, seq_lens,
+               (("v_cache", v_cache, torch.bfloat16, shape),), q, page_table, seq_lens,
                sm_scale, (int(window), int(sinks)), out, lse, workspace, abort, num_ctas, stream)
 
 
@@ -716,7 +713,7 @@ def paged_decode_attn_int4_window(q, k_codes, k_params, v_codes, v_params, page_
     """paged_decode_attn_int4 over the last `window` and the first `sinks` tokens."""
     pools = (k_codes, k_params, v_codes, v_params)
     shape = _int4_shape(k_codes)
-    _attn_call("paged_decode_attn_int4_window", pools, (), shape, _int4_specs(shape, *pools), q,
+    _attn_call("paged_decode_attn_int4_window", pools, (), shape, _int4_specs(shape, *pools[1:]), q,
                page_table, seq_lens, sm_scale, (int(window), int(sinks)), out, lse, workspace,
                abort, num_ctas, stream)
 

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -51,8 +52,9 @@ struct DeviceInfo {
     int sms = 0;
     // [cache type][d128][gp16][two KV heads per item][window]
     int occupancy[3][2][2][2][2] = {};
-    // resident clusters of each size (index = cluster size; -1 = not queried)
-    int clusters[3][2][2][2][2][pkv::kMaxCluster + 1];
+    // resident clusters of each size (index = cluster size; -1 = not queried);
+    // read without the lock
+    mutable std::atomic<int> clusters[3][2][2][2][2][pkv::kMaxCluster + 1];
 };
 std::mutex g_dev_mutex;
 DeviceInfo g_dev[kMaxDevices];
@@ -95,15 +97,11 @@ pkv::AttnVariant variant_of(int kv, int head_dim, int group, int kv_per_item, bo
 
 // Clusters of `size` CTAs of this attention variant that fit on the device at
 // once (queried once per device, variant and size).
-pkv_status max_clusters(const pkv::AttnVariant& v, int size, int* out) {
-    const DeviceInfo* cinfo = nullptr;
-    pkv_status st = device_info(&cinfo);
-    if (st != PKV_OK) return st;
-    DeviceInfo& info = const_cast<DeviceInfo&>(*cinfo);
-    std::lock_guard<std::mutex> lock(g_dev_mutex);
-    int& slot = info.clusters[v.kv][v.head_dim == 128][v.group_pad == 16][v.kv_per_item == 2]
-                             [v.window][size];
+int max_clusters(const DeviceInfo& info, const pkv::AttnVariant& v, int size) {
+    std::atomic<int>& slot =
+        info.clusters[v.kv][v.head_dim == 128][v.group_pad == 16][v.kv_per_item == 2][v.window][size];
     if (slot < 0) {
+        std::lock_guard<std::mutex> lock(g_dev_mutex);
         int n = 0;
         cudaError_t e = pkv::attn_max_clusters(v, size, &n);
         if (e != cudaSuccess) {
@@ -112,8 +110,7 @@ pkv_status max_clusters(const pkv::AttnVariant& v, int size, int* out) {
         }
         slot = n;
     }
-    *out = slot;
-    return PKV_OK;
+    return slot;
 }
 
 // Cluster mode for `items` work items: cluster size C and K clusters, each
@@ -127,13 +124,14 @@ pkv_status choose_clusters(const pkv::AttnVariant& v, int64_t items, int forced,
                            int* count) {
     *size = 0;
     *count = 0;
+    const DeviceInfo* info = nullptr;
+    pkv_status st = device_info(&info);
+    if (st != PKV_OK) return st;
     double best = 0.0;
     const int c_lo = forced > 0 ? forced : 2;
     const int c_hi = forced > 0 ? forced : pkv::kMaxCluster;
     for (int c = c_lo; c <= c_hi; ++c) {
-        int kmax = 0;
-        pkv_status st = max_clusters(v, c, &kmax);
-        if (st != PKV_OK) return st;
+        const int kmax = max_clusters(*info, v, c);
         if (kmax <= 0) continue;
         const int64_t k = std::min<int64_t>(items, kmax);
         const int64_t per = (items + k - 1) / k;            // items of the fullest cluster
@@ -308,9 +306,7 @@ pkv_status model_split(int kv, int head_dim, int group, bool window, int page_si
         const int64_t parts = items * (wide / heads);
         const pkv::AttnVariant v = variant_of(kv, head_dim, group, heads, window);
         for (int c = 1; c <= pkv::kMaxCluster; ++c) {
-            int kmax = 0;
-            st = max_clusters(v, c, &kmax);
-            if (st != PKV_OK) return st;
+            const int kmax = max_clusters(*info, v, c);
             if (kmax <= 0) continue;
             const int64_t k = std::min<int64_t>(parts, kmax);
             const int64_t most = (parts + k - 1) / k;   // items of the fullest cluster
