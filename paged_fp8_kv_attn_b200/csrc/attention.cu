@@ -1120,10 +1120,11 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // are held relative to m (0 before the first visible token, when `bound`
         // lets every score raise it).
         float vref = 0.f, vinv = 0.f, vbias[kNB][C::kGroups][2], bound = kNegInf;
+        float neg[kNB][4];   // -m as the accumulator of the scores: columns 2c, 2c + 1, twice
         if constexpr (kInt4) {
 #pragma unroll
             for (int nb = 0; nb < kNB; ++nb) {
-                m[nb][0] = m[nb][1] = 0.f;
+                neg[nb][0] = neg[nb][1] = neg[nb][2] = neg[nb][3] = 0.f;
 #pragma unroll
                 for (int gr = 0; gr < C::kGroups; ++gr) vbias[nb][gr][0] = vbias[nb][gr][1] = 0.f;
             }
@@ -1162,10 +1163,6 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         uint32_t x[4];
                         ldsm_x4(kb4 + k4_off[gr] + trow[t] * C::kRowBytes, x[0], x[1], x[2], x[3]);
 #pragma unroll
-                        for (int nb = 0; nb < kNB; ++nb)
-                            acc[t][nb][gr][0] = acc[t][nb][gr][1] = acc[t][nb][gr][2] =
-                                acc[t][nb][gr][3] = 0.f;
-#pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t msk = (i & 1) ? 0x00F000F0u : 0x000F000Fu;
                             if (i == 2) {
@@ -1173,9 +1170,15 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                 for (int k = 0; k < 4; ++k) x[k] >>= 8;
                             }
 #pragma unroll
-                            for (int nb = 0; nb < kNB; ++nb)
-                                mma_f16(acc[t][nb][gr], x[0] & msk, x[1] & msk, x[2] & msk, x[3] & msk,
-                                        qb[nb][4 * gr + i][0], qb[nb][4 * gr + i][1]);
+                            for (int nb = 0; nb < kNB; ++nb) {
+                                const uint32_t b0 = qb[nb][4 * gr + i][0], b1 = qb[nb][4 * gr + i][1];
+                                if (i == 0)
+                                    mma_f16_first(acc[t][nb][gr], x[0] & msk, x[1] & msk, x[2] & msk,
+                                                  x[3] & msk, b0, b1);
+                                else
+                                    mma_f16(acc[t][nb][gr], x[0] & msk, x[1] & msk, x[2] & msk,
+                                            x[3] & msk, b0, b1);
+                            }
                         }
                     }
                 }
@@ -1209,8 +1212,8 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     }
 #pragma unroll
                     for (int nb = 0; nb < kNB; ++nb) {
-                        float y[4] = {-m[nb][0], -m[nb][1], -m[nb][0], -m[nb][1]};
-                        mma_bf16(y, kw[0], kw[1], kw[0], kw[1], qy[nb][0], qy[nb][1]);
+                        float y[4];
+                        mma_bf16_first(y, kw[0], kw[1], kw[0], kw[1], qy[nb][0], qy[nb][1], neg[nb]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float x = ks[e >> 1][0] * acc[t][nb][0][e];
@@ -1271,7 +1274,8 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             // m rises; the first visible scores set it either way
                             up = (up == kNegInf) ? 0.f : (bound == kNegInf ? up : fmaxf(up, 0.f));
                             alpha[col] = bound == kNegInf ? 0.f : exp2f(-up);
-                            m[nb][col] += up;
+                            neg[nb][col] -= up;
+                            neg[nb][col + 2] = neg[nb][col];
                             l[nb][col] *= alpha[col];
 #pragma unroll
                             for (int gr = 0; gr < C::kGroups; ++gr) vbias[nb][gr][col] *= alpha[col];
@@ -1547,10 +1551,11 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         int next_aborted = 0;
         if constexpr (C::kEarlyQ) next_aborted = have_next ? load_q(sn, qw) : 0;
         if constexpr (kInt4) {
-            if (bound == kNegInf) {   // no visible token: a partial of weight zero
 #pragma unroll
-                for (int nb = 0; nb < kNB; ++nb) m[nb][0] = m[nb][1] = kNegInf;
-            }
+            for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+                for (int col = 0; col < 2; ++col)   // (no visible token: a partial of weight zero)
+                    m[nb][col] = bound == kNegInf ? kNegInf : -neg[nb][col];
         }
         const bool whole = whole_of();
         const int64_t head0 = head0_of();
