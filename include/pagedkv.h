@@ -301,6 +301,8 @@ PKV_API pkv_status kv_read_slots_int4(const int32_t* slot_map, int32_t num_token
  *    and behind the last token.
  * The caller checks failed (and cu_tokens[batch] <= max_tokens) when it reads
  * the step's results; pages go back by being pushed onto the stack.
+ * Calls that share a stack or page-table rows are to be ordered, as on one
+ * stream.
  * old_lens, new_lens [batch]; free_pages [free_capacity], free_capacity <=
  * num_pages; page_table and expected_tags [batch][max_pages]; slot_map
  * [max_tokens]; cu_tokens [batch + 1]; failed [batch] uint8.  Apart from

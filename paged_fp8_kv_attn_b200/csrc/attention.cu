@@ -575,7 +575,12 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
     }
     __syncthreads();
-    if (u_lo >= u_hi && !clu) return;   // nothing to do (the merge reads no slot of this CTA)
+    if (u_lo >= u_hi && !clu) {   // nothing to do (the merge reads no slot of this CTA)
+        // (a batch with no unit at all must not finish before the kernel in front of
+        // it, or the kernels behind it would take that one for finished)
+        grid_dependency_wait();
+        return;
+    }
     // (an empty range in cluster mode: the walk yields nothing and the CTA
     // only takes part in its cluster's reduction)
     walk.init(u_lo < u_hi ? scratch[8] : 0, u_lo < u_hi ? scratch[9] : 0, u_lo, u_hi);

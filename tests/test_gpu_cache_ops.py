@@ -348,7 +348,7 @@ def attention_case(kind, lens, G, H, D, P, seed, spare=3, extra_pages=2):
     rng = np.random.Generator(np.random.PCG64(seed))
     lens = np.asarray(lens, np.int32)
     B = lens.size
-    used = [max(0, -(-int(n) // P)) for n in lens]
+    used = [max(0, -(-int(n) // P)) if n < 10**5 else 0 for n in lens]
     MP = max(used) + extra_pages
     NP = sum(used) + spare
     perm = rng.permutation(NP).astype(np.int32)
@@ -458,6 +458,32 @@ def test_int4_attention_long_request(cuda_device):
     p, q, table, lens = attention_case("int4", [40001], 8, 2, 128, 64, seed=6)
     run_attention(p, q, table, lens, ctas=(0, 1, 148, 296, -16))
     run_attention(p, q, table, lens, window=30011, sinks=100, ctas=(0, 296, -8))
+
+
+def test_int4_work_split_choice(cuda_device):
+    """Short requests: one launch, clusters of one CTA; long ones on few items: split-K.
+    The choice is one of the splits that the other tests run."""
+    size, ctas, launches = pkv.paged_decode_attn_plan(pkv.PKV_KV_INT4, 128, 64, 8, 128, 1, 16)
+    assert (size, launches) == (1, 1) and ctas >= 128
+    size, ctas, launches = pkv.paged_decode_attn_plan(pkv.PKV_KV_INT4, 2, 32, 8, 128, 1024, 128)
+    assert (size, launches) == (0, 2) and ctas >= 148
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attention_of_a_batch_without_requests(cuda_device, kind):
+    """Every request padded (length 0) or invalid, by every work split: dead outputs, and
+    the calls around it keep their order."""
+    p, q, table, lens = attention_case(kind, [0, -1, 0, 10**6, 0], 4, 2, 64, 16, seed=2,
+                                       extra_pages=3, spare=9)
+    c = Cache(p)
+    gq, gt, gl = cuda(q), cuda(table[:, :3].copy()), cuda(lens)
+    for window in (0, 20):
+        for n in (0, 1, 40, -1, -2):
+            out, lse = c.attend(gq, gt, gl, 0.1, c.workspace(5, 8, n), window, 2 if window else 0,
+                                num_ctas=n) if kind == "int4" or window else (None, None)
+            if out is not None:
+                torch.cuda.synchronize()
+                assert not out.any() and torch.isneginf(lse).all()
 
 
 @pytest.mark.parametrize("kind", ["int4", "bf16"])
