@@ -1,24 +1,27 @@
 // kv_slots.cu -- token writes into cache slots named by a slot map, and reads
 // of such slots back as bf16, for FP8, BF16 and INT4 caches.
 //
-// A warp moves the K rows or the V rows of `tokens` consecutive tokens, as many
-// as make kInFlight 8-value blocks (16 bytes of bf16) for each lane, at least
-// one: 32 consecutive blocks at a time are 512 bytes of one row, or whole short
-// rows, and an INT4 group of 64 dims is 8 consecutive lanes, whose minimum and
-// maximum meet in three shuffles.  Nothing is read twice, so memory bounds large
-// calls, and the chain of two dependent loads, slot then row, small ones: a
-// lane's kInFlight blocks are loaded together, and K and V are different warps.
+// A warp moves the K row or the V row of a token, 32 consecutive 8-value blocks
+// (16 bytes of bf16) at a time, or of as many consecutive tokens as fill its
+// lanes; an INT4 group of 64 dims is 8 consecutive lanes, whose minimum and maximum
+// meet in three shuffles.  Nothing is read twice, so memory bounds large calls,
+// and the chain of two dependent loads, slot then row, small ones: up to four
+// blocks of a long row are in a lane's flight together, and K and V are different
+// warps.  (More rows a warp for more blocks in flight made short rows slower:
+// 20,000 tokens of 1 x 64, INT4 6.0 us with four, 4.4 with one.)
 #include "kv_codec.cuh"
 
 namespace pkv {
 
 constexpr int kSlotThreads = 256;
 constexpr int kSlotWarps = kSlotThreads / 32;
-constexpr int kInFlight = 4;
+// blocks of a lane in flight
+template <bool kOne>
+constexpr int kFlight = kOne ? 4 : 1;
 
 // The calling warp's part of a call: blocks [0, total) of its tokens' rows.
-// kOne: a single token, whose slot is loaded and resolved once (measured: half
-// the time of a long row's write, 2 us of 10 of its read).
+// kOne: a single token, whose slot is loaded and resolved once (8,192 tokens of
+// 8 x 128, INT4: write 16.6 us, read 9.4; block by block 18.8 and 11.7).
 template <int kD, bool kOne>
 struct SlotWork {
     const SlotArgs& a;
@@ -41,8 +44,7 @@ struct SlotWork {
         shift = 31 - __clz(a.page_size);
         row0 = kOne && total > 0 ? row_of(a.slot_map[token0]) : -1;
     }
-    // The token (from token0) of block u.  (tokens * blocks is at most 32 kInFlight,
-    // and u times inv's excess below 2^16.)
+    // The token (from token0) of block u < 32 (u times inv's excess is below 2^16).
     __device__ __forceinline__ int token_of(int u) const {
         return kOne ? 0 : static_cast<int>((u * inv) >> 16);
     }
@@ -65,6 +67,7 @@ write_slots_kernel(const KvDst dst, const uint16_t* __restrict__ k_new,
                    const uint16_t* __restrict__ v_new, const SlotArgs a, int tokens) {
     launch_dependents();
     grid_dependency_wait();
+    constexpr int kInFlight = kFlight<kOne>;
     const SlotWork<kD, kOne> w(a, tokens);
     if (kOne && w.row0 < 0) return;
     const int64_t stride = w.is_v ? a.v_stride : a.k_stride;
@@ -101,6 +104,7 @@ read_slots_kernel(const KvDst src, uint16_t* __restrict__ k_out, uint16_t* __res
                   const SlotArgs a, int tokens) {
     launch_dependents();
     grid_dependency_wait();
+    constexpr int kInFlight = kFlight<kOne>;
     const SlotWork<kD, kOne> w(a, tokens);
     const int64_t stride = w.is_v ? a.v_stride : a.k_stride;
     uint16_t* const out = (w.is_v ? v_out : k_out) + w.token0 * stride;
@@ -131,10 +135,9 @@ read_slots_kernel(const KvDst src, uint16_t* __restrict__ k_out, uint16_t* __res
     }
 }
 
-// A warp takes as many whole rows as fill its lanes kInFlight times.
 static int slot_tokens(const SlotArgs& a) {
     const int blocks = a.num_kv_heads * (a.head_dim / 8);
-    return blocks >= 32 * kInFlight ? 1 : 32 * kInFlight / blocks;
+    return blocks >= 32 ? 1 : 32 / blocks;
 }
 
 template <typename K, typename... A>
