@@ -58,6 +58,12 @@ constexpr int kConsumerThreads = kConsumerWarps * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;
+// INT4 holds weights times scales in f16, below 2^12 * 8: scores may pass the running
+// maximum by 12, which most never do after a segment's first tokens, and a scale the
+// reference vref by 8 (against 8 and 64: 64 x 8,192 tokens 131.0 us of 132.3, groups of
+// 16 heads 78.8 of 80.9).
+constexpr float kInt4RescaleThreshold = 12.0f;
+constexpr float kInt4ScaleSpan = 8.0f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 template <int kKv, int kD, int kGP, int kH>
@@ -1252,7 +1258,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     for (int gr = 0; gr < C::kGroups; ++gr)
                         vtop = fmaxf(vtop, fmaxf(fabsf(vs[t][0][gr]), fabsf(vs[t][1][gr])));
                 }
-                if (__any_sync(0xffffffffu, ptop > bound || vtop > 64.f * vref)) {
+                if (__any_sync(0xffffffffu, ptop > bound || vtop > kInt4ScaleSpan * vref)) {
                     // the largest scale so far as a power of two, within [2^-100, 2^126]
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1)
@@ -1299,11 +1305,11 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             o[nb][mb][3] *= alpha[1];
                         }
                     }
-                    if (__any_sync(0xffffffffu, any)) bound = kRescaleThreshold;
+                    if (__any_sync(0xffffffffu, any)) bound = kInt4RescaleThreshold;
                 }
                 // (4) weights, and O^T[16 dims][8 heads] += V^T P^T.  The f16 weight of
-                // a group is w scale / vref: w is at most 2^8 and scale / vref below
-                // 64, so it stays below 2^14.  After the transposing load the low
+                // a group is w scale / vref: w is at most 2^12 and scale / vref at most
+                // 8, so it stays within 2^15.  After the transposing load the low
                 // (high) halves of a word are two tokens' dims 4g .. 4g + 3: m-block
                 // 2 gr' + i takes nibble 2i (accumulator rows g, code * 2^-24) and
                 // 2i + 1 (rows g + 8, code * 2^-20).  Masked tokens have zero weights,
