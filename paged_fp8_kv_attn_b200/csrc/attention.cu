@@ -1317,11 +1317,15 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 // (4) weights, and O^T[16 dims][8 heads] += V^T P^T.  The f16 weight of
                 // a group is w scale / vref: w is at most 2^12 and scale / vref at most
-                // 8, so it stays within 2^15.  After the transposing load the low
-                // (high) halves of a word are two tokens' dims 4g .. 4g + 3: m-block
-                // 2 gr' + i takes nibble 2i (accumulator rows g, code * 2^-24) and
-                // 2i + 1 (rows g + 8, code * 2^-20).  Masked tokens have zero weights,
-                // and every code is a finite number.
+                // 8, so it stays within 2^15.  Its rounding, 2^-11 at most of
+                // w scale code, is the price of f16 products; the minima's part and the
+                // sum of the weights keep 32 bits.  (Over 10,121 random calls the bf16
+                // output is off by at worst 2.7e-3 of its norm, against 1.8e-3 for
+                // binary32 weights on the same call.)  After the transposing
+                // load the low (high) halves of a word are two tokens' dims
+                // 4g .. 4g + 3: m-block 2 gr' + i takes nibble 2i (accumulator rows g,
+                // code * 2^-24) and 2i + 1 (rows g + 8, code * 2^-20).  Masked tokens
+                // have zero weights, and every code is a finite number.
 #pragma unroll
                 for (int t = 0; t < kH; ++t) {
                     uint32_t pb[kNB][C::kGroups][2];
