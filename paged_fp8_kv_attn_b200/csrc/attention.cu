@@ -64,11 +64,6 @@ constexpr float kRescaleThreshold = 8.0f;
 // 16 heads 78.8 of 80.9).
 constexpr float kInt4RescaleThreshold = 12.0f;
 constexpr float kInt4ScaleSpan = 8.0f;
-// INT4 consumers release stage s through named barrier kStageBarrier + s instead of
-// an mbarrier, on which the waiting producer's polls would take a tenth of the issue
-// slots (groups of 16 heads 76.9 us of 79.0).  The wait needs no limit: every consumer
-// warp arrives for every stage, also after a wait of its own has expired.
-constexpr int kStageBarrier = 2;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 template <int kKv, int kD, int kGP, int kH>
@@ -125,7 +120,6 @@ struct AttnCfg {
     static constexpr int kRecOff = (kCluOff + kCluInts * 4 + 15) / 16 * 16;
     static constexpr int kSmemBytes = kRecOff + kRecBytes + 1024;  // + alignment slack
     static_assert(kRecBytes <= kStageBytes, "a record must fit in one stage");
-    static_assert(kStageBarrier + kStages <= 16, "a CTA has 16 named barriers");
     // Registers per thread holding a segment's raw query words.  They are
     // loaded before the previous segment's epilogue when that adds at most
     // 16 live registers to a variant with the 2-CTA register budget (168);
@@ -708,8 +702,12 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const uint32_t use = __ballot_sync(0xffffffffu, wanted && known);
                 const bool bad = __any_sync(0xffffffffu, wanted && !known);
                 const int32_t y = (pid * Hkv + sg.h * kH) << pshift;   // first pool row
-                if (iter >= static_cast<uint32_t>(S))
-                    named_barrier_sync(kStageBarrier + stage, kAttnThreads);
+                if (iter >= static_cast<uint32_t>(S)) {
+                    if (lane == 0)
+                        wait_or_give_up(&empty_bar[stage], ((iter / S) + 1) & 1, cta_failed,
+                                        a.ws_status);
+                    __syncwarp();
+                }
                 const uint32_t kdst = smem_addr(smem + stage * C::kStageBytes);
                 if (lane == 0) {
                     stage_bad[stage] = bad;
@@ -776,14 +774,8 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             for (int ch = s.c0; ch < s.c1 && !direct; ++ch, ++it) {
                 const int stage = it % S;
                 if (it >= static_cast<uint32_t>(S)) {
-                    if constexpr (kInt4) {
-                        named_barrier_sync(kStageBarrier + stage, kAttnThreads);
-                    } else {
-                        if (lane == 0)
-                            wait_or_give_up(&empty_bar[stage], ((it / S) + 1) & 1, cta_failed,
-                                            a.ws_status);
-                        __syncwarp();
-                    }
+                    if (lane == 0) wait_or_give_up(&empty_bar[stage], ((it / S) + 1) & 1, cta_failed, a.ws_status);
+                    __syncwarp();
                 }
                 const uint32_t kdst = smem_addr(smem + stage * C::kStageBytes);
                 const uint32_t vdst = kdst + C::kTileBytes;
@@ -1567,12 +1559,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }   // tiles
             }
             __syncwarp();
-            if constexpr (kInt4) {
-                if (!(C::kRedInStage && ch + 1 == s.c1))
-                    named_barrier_arrive(kStageBarrier + stage, kAttnThreads);
-            } else if (lane == 0 && !(C::kRedInStage && ch + 1 == s.c1)) {
-                mbar_arrive(&empty_bar[stage]);
-            }
+            if (lane == 0 && !(C::kRedInStage && ch + 1 == s.c1)) mbar_arrive(&empty_bar[stage]);
         }
         // the next segment's query words and abort flag, consumed after the
         // epilogue
@@ -1747,11 +1734,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // generic-proxy writes to it: order them first
         if constexpr (C::kRedInStage) fence_proxy_async_smem();
         named_barrier_sync(1, kConsumerThreads);
-        if constexpr (kInt4) {
-            if (C::kRedInStage) named_barrier_arrive(kStageBarrier + last_stage, kAttnThreads);
-        } else if (C::kRedInStage && lane == 0) {
-            mbar_arrive(&empty_bar[last_stage]);
-        }
+        if (C::kRedInStage && lane == 0) mbar_arrive(&empty_bar[last_stage]);
         if constexpr (C::kEarlyQ) aborted = next_aborted;
         s = sn;
         have = have_next;
