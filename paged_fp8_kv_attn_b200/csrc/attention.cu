@@ -38,8 +38,9 @@
 //    each thread's shared-memory reads are 16-byte (K) or 4-byte (V) words
 //    that hit 32 distinct banks under the TMA swizzle.
 //  * Lazy rescaling: a warp rescales O only when a head's running maximum
-//    grows by more than 8 (log2 units); P is then at most 2^8, exact enough
-//    in f16 and far from overflow.
+//    grows by more than 8 (log2 units; INT4: 12); P is then at most 2^8,
+//    exact enough in f16 and far from overflow.  INT4's f16 weights, P times a
+//    scale, have a reference of their own.
 //  * INT4: a value is s code + m per token and group of 64 dims, so
 //    q . k = sum_groups s (q . code) + m sum(q), and the weighted sum of V is
 //    sum (w s) code + sum w m.  The products run over the codes as they lie in
@@ -58,12 +59,16 @@ constexpr int kConsumerThreads = kConsumerWarps * 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;
-// INT4 holds weights times scales in f16, below 2^12 * 8: scores may pass the running
-// maximum by 12, which most never do after a segment's first tokens, and a scale the
-// reference vref by 8 (against 8 and 64: 64 x 8,192 tokens 131.0 us of 132.3, groups of
-// 16 heads 78.8 of 80.9).
+// INT4: scores may pass the running maximum by 12, which most never do after a segment's
+// first tokens (against 8: 64 x 8,192 tokens 131.0 us of 132.3, groups of 16 heads 78.8 of
+// 80.9).  Weights times scales are held in f16 relative to a power of two per head and
+// group that puts the largest so far at 8 to 16 when it is set, and again when one passes
+// kInt4WeightMax: twelve octaves for the scores' rise, and 2^-28 of the largest at the
+// small end.
 constexpr float kInt4RescaleThreshold = 12.0f;
-constexpr float kInt4ScaleSpan = 8.0f;
+constexpr float kInt4WeightMax = 32768.0f;
+constexpr uint32_t kInt4WeightSet = 257u;   // exponent fields: inverse + largest (2^3)
+constexpr uint32_t kInt4InvTop = 227u;      // exponent field of the largest inverse (2^100)
 constexpr float kNegInf = -__builtin_huge_valf();
 
 template <int kKv, int kD, int kGP, int kH>
@@ -256,6 +261,11 @@ struct Walker {
         return true;
     }
 };
+
+// 2^k for k <= 0, as an unsigned difference (0 below 2^-126).
+__device__ __forceinline__ float octave(uint32_t k) {
+    return __int_as_float(max(127 + static_cast<int>(k), 0) << 23);
+}
 
 // Bounded mbarrier wait.  After a timeout in this CTA every later wait
 // returns at once, so the kernel always runs to completion; the workspace
@@ -1125,19 +1135,24 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             l[nb][0] = l[nb][1] = 0.f;
             lr[nb][0] = lr[nb][1] = 0.f;
         }
-        // INT4: O holds sum_t w_t s_t code_t / vref, with vref (a power of two,
-        // common to the warp) keeping the f16 weights w_t s_t / vref in range, and
-        // vbias the part of the groups' minima, sum_t w_t m_t, in binary32.  Scores
-        // are held relative to m (0 before the first visible token, when `bound`
-        // lets every score raise it).
-        float vref = 0.f, vinv = 0.f, vbias[kNB][C::kGroups][2], bound = kNegInf;
+        // INT4: O holds sum_t w_t s_t code_t vinv, with vinv, a power of two per
+        // head and group, keeping the f16 weights w_t s_t vinv in range, and vbias
+        // the part of the groups' minima, sum_t w_t m_t, in binary32.  (Per head
+        // and group, and by w s rather than s: where one head's weight lies on a
+        // large scale, or one group's scales are large, the others keep their bits.)
+        // Scores are held relative to m (0 before the first visible token, when
+        // `bound` lets every score raise it).
+        float vinv[kNB][C::kGroups][2], vbias[kNB][C::kGroups][2], bound = kNegInf;
         float neg[kNB][4];   // -m as the accumulator of the scores: columns 2c, 2c + 1, twice
         if constexpr (kInt4) {
 #pragma unroll
             for (int nb = 0; nb < kNB; ++nb) {
                 neg[nb][0] = neg[nb][1] = neg[nb][2] = neg[nb][3] = 0.f;
 #pragma unroll
-                for (int gr = 0; gr < C::kGroups; ++gr) vbias[nb][gr][0] = vbias[nb][gr][1] = 0.f;
+                for (int gr = 0; gr < C::kGroups; ++gr) {
+                    vbias[nb][gr][0] = vbias[nb][gr][1] = 0.f;
+                    vinv[nb][gr][0] = vinv[nb][gr][1] = 0x1p100f;
+                }
             }
         }
         int poisoned = 0;
@@ -1199,7 +1214,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 // [2..3]: row g + 8.
                 float p[kH][kNB][4];
                 float vs[kH][2][C::kGroups], vm[kH][2][C::kGroups];   // V's of rows g, g + 8
-                float vtop = 0.f, ptop = kNegInf;
+                float ptop = kNegInf;
                 const uint32_t par = vb4 + C::kTileBytes + g * kPR;
 #pragma unroll
                 for (int t = 0; t < kH; ++t) {
@@ -1247,31 +1262,18 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                 for (int gr = 0; gr < C::kGroups; ++gr) vs[t][i][gr] = vm[t][i][gr] = 0.f;
                             }
                 }
-                // (3) lazy rescaling, as below, and of vref with V's scales
+                // (3) lazy rescaling, as below, by whole octaves: m rises, and O keeps
+                // its value with vinv risen alike (past 2^100, O falls instead)
 #pragma unroll
-                for (int t = 0; t < kH; ++t) {
+                for (int t = 0; t < kH; ++t)
 #pragma unroll
                     for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) ptop = fmaxf(ptop, p[t][nb][e]);
-#pragma unroll
-                    for (int gr = 0; gr < C::kGroups; ++gr)
-                        vtop = fmaxf(vtop, fmaxf(fabsf(vs[t][0][gr]), fabsf(vs[t][1][gr])));
-                }
-                if (__any_sync(0xffffffffu, ptop > bound || vtop > kInt4ScaleSpan * vref)) {
-                    // the largest scale so far as a power of two, within [2^-100, 2^126]
-#pragma unroll
-                    for (int off = 4; off < 32; off <<= 1)
-                        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
-                    const uint32_t ve = min(max(__float_as_uint(vtop) >> 23, 27u), 253u);
-                    const float now = fmaxf(vref, __uint_as_float(ve << 23));
-                    vinv = __uint_as_float((254u - (__float_as_uint(now) >> 23)) << 23);
-                    const float vfix = vref * vinv;
-                    vref = now;
+                if (__any_sync(0xffffffffu, ptop > bound)) {
                     bool any = false;
 #pragma unroll
-                    for (int nb = 0; nb < kNB; ++nb) {
-                        float alpha[2];
+                    for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
                         for (int col = 0; col < 2; ++col) {
                             float up = kNegInf;   // the largest score less m
@@ -1282,66 +1284,115 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
                             up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16));
                             any |= up != kNegInf;
-                            // m rises; the first visible scores set it either way
-                            up = (up == kNegInf) ? 0.f : (bound == kNegInf ? up : fmaxf(up, 0.f));
-                            alpha[col] = bound == kNegInf ? 0.f : exp2f(-up);
+                            // the first visible scores set m either way
+                            const bool first = bound == kNegInf;
+                            up = (up == kNegInf) ? 0.f : (first ? up : ceilf(fmaxf(up, 0.f)));
+                            const float alpha = first ? 0.f : exp2f(-up);
+                            const uint32_t octaves = first ? 0u : static_cast<uint32_t>(fminf(up, 512.f));
                             neg[nb][col] -= up;
                             neg[nb][col + 2] = neg[nb][col];
-                            l[nb][col] *= alpha[col];
+                            l[nb][col] *= alpha;
 #pragma unroll
-                            for (int gr = 0; gr < C::kGroups; ++gr) vbias[nb][gr][col] *= alpha[col];
-                            alpha[col] *= vfix;
+                            for (int gr = 0; gr < C::kGroups; ++gr) {
+                                vbias[nb][gr][col] *= alpha;
+                                const uint32_t e = (__float_as_uint(vinv[nb][gr][col]) >> 23) + octaves;
+                                const uint32_t now = min(e, kInt4InvTop);
+                                vinv[nb][gr][col] = __uint_as_float(now << 23);
+                                const float fall = octave(now - e);
+#pragma unroll
+                                for (int mb = 4 * gr; mb < 4 * gr + 4; ++mb) {
+                                    o[nb][mb][col] *= fall;
+                                    o[nb][mb][col + 2] *= fall;
+                                }
+                            }
 #pragma unroll
                             for (int t = 0; t < kH; ++t) {
                                 p[t][nb][col] -= up;
                                 p[t][nb][col + 2] -= up;
                             }
                         }
-#pragma unroll
-                        for (int mb = 0; mb < kMB; ++mb) {
-                            o[nb][mb][0] *= alpha[0];
-                            o[nb][mb][1] *= alpha[1];
-                            o[nb][mb][2] *= alpha[0];
-                            o[nb][mb][3] *= alpha[1];
-                        }
-                    }
                     if (__any_sync(0xffffffffu, any)) bound = kInt4RescaleThreshold;
                 }
-                // (4) weights, and O^T[16 dims][8 heads] += V^T P^T.  The f16 weight of
-                // a group is w scale / vref: w is at most 2^12 and scale / vref at most
-                // 8, so it stays within 2^15.  Its rounding, 2^-11 at most of
-                // w scale code, is the price of f16 products; the minima's part and the
-                // sum of the weights keep 32 bits.  (Over 10,121 random calls the bf16
-                // output is off by at worst 2.7e-3 of its norm, against 1.8e-3 for
-                // binary32 weights on the same call.)  After the transposing
+                // (4) weights: their sum and the minima's part in binary32, and w scale
+                // vinv as f16 pairs.  The pairs' rounding, 2^-11 at most of w scale code
+                // (below 2^-17 of the head's and group's largest w scale so far in this
+                // warp's segment: 2^-28 of that), is the price of f16 products.  (Over
+                // 13,681 random calls the bf16 output's error is at worst 2.5 times that
+                // of binary32 weights, 2.5e-3 of its norm against 1.0e-3.)
+#pragma unroll
+                for (int t = 0; t < kH; ++t)
+#pragma unroll
+                    for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            p[t][nb][e] = ex2_approx(p[t][nb][e]);
+                            l[nb][e & 1] += p[t][nb][e];
+#pragma unroll
+                            for (int gr = 0; gr < C::kGroups; ++gr)
+                                vbias[nb][gr][e & 1] =
+                                    fmaf(p[t][nb][e], vm[t][e >> 1][gr], vbias[nb][gr][e & 1]);
+                        }
+                uint32_t pw[kH][kNB][C::kGroups][2];
+                // (w scale before vinv, whose product with a scale might pass binary32)
+                auto weigh = [&]() {
+                    float top = 0.f;
+#pragma unroll
+                    for (int t = 0; t < kH; ++t)
+#pragma unroll
+                        for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+                            for (int gr = 0; gr < C::kGroups; ++gr)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const float x = p[t][nb][2 * i] * vs[t][i][gr] * vinv[nb][gr][0];
+                                    const float y = p[t][nb][2 * i + 1] * vs[t][i][gr] * vinv[nb][gr][1];
+                                    top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
+                                    pw[t][nb][gr][i] = pack_f16x2(x, y);
+                                }
+                    return top;
+                };
+                if (__any_sync(0xffffffffu, weigh() > kInt4WeightMax)) {
+#pragma unroll
+                    for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+                        for (int gr = 0; gr < C::kGroups; ++gr)
+#pragma unroll
+                            for (int col = 0; col < 2; ++col) {
+                                float top = 0.f;
+#pragma unroll
+                                for (int t = 0; t < kH; ++t)
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i)
+                                        top = fmaxf(top, fabsf(p[t][nb][2 * i + col] * vs[t][i][gr]));
+#pragma unroll
+                                for (int off = 4; off < 32; off <<= 1)
+                                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                                const uint32_t e = __float_as_uint(vinv[nb][gr][col]) >> 23;
+                                const uint32_t now = min(e, kInt4WeightSet - (__float_as_uint(top) >> 23));
+                                vinv[nb][gr][col] = __uint_as_float(now << 23);
+                                const float fall = octave(now - e);
+#pragma unroll
+                                for (int mb = 4 * gr; mb < 4 * gr + 4; ++mb) {
+                                    o[nb][mb][col] *= fall;
+                                    o[nb][mb][col + 2] *= fall;
+                                }
+                            }
+                    weigh();
+                }
+                // (5) O^T[16 dims][8 heads] += V^T P^T.  After the transposing
                 // load the low (high) halves of a word are two tokens' dims
                 // 4g .. 4g + 3: m-block 2 gr' + i takes nibble 2i (accumulator rows g,
                 // code * 2^-24) and 2i + 1 (rows g + 8, code * 2^-20).  Masked tokens
                 // have zero weights, and every code is a finite number.
 #pragma unroll
                 for (int t = 0; t < kH; ++t) {
-                    uint32_t pb[kNB][C::kGroups][2];
 #pragma unroll
-                    for (int nb = 0; nb < kNB; ++nb) {
+                    for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            p[t][nb][e] = ex2_approx(p[t][nb][e]);
-                            l[nb][e & 1] += p[t][nb][e];
-                        }
+                        for (int gr = 0; gr < C::kGroups; ++gr)
 #pragma unroll
-                        for (int gr = 0; gr < C::kGroups; ++gr) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const float w = vs[t][i][gr] * vinv;
-                                pb[nb][gr][i] = movmatrix_trans(
-                                    pack_f16x2(p[t][nb][2 * i] * w, p[t][nb][2 * i + 1] * w));
-#pragma unroll
-                                for (int col = 0; col < 2; ++col)
-                                    vbias[nb][gr][col] =
-                                        fmaf(p[t][nb][2 * i + col], vm[t][i][gr], vbias[nb][gr][col]);
-                            }
-                        }
-                    }
+                            for (int i = 0; i < 2; ++i)
+                                pw[t][nb][gr][i] = movmatrix_trans(pw[t][nb][gr][i]);
 #pragma unroll
                     for (int gr = 0; gr < C::kGroups; ++gr) {
                         // x[0], x[1]: tokens 2c, 2c+1, dims 4g.. of the halves; x[2], x[3]:
@@ -1358,7 +1409,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                 for (int nb = 0; nb < kNB; ++nb)
                                     mma_f16(o[nb][4 * gr + 2 * half + k], lo & 0x000F000Fu,
                                             lo & 0x00F000F0u, hi & 0x000F000Fu, hi & 0x00F000F0u,
-                                            pb[nb][gr][0], pb[nb][gr][1]);
+                                            pw[t][nb][gr][0], pw[t][nb][gr][1]);
                             }
                     }
                 }
@@ -1648,6 +1699,8 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                 const float* x = o[nb][4 * gr + 2 * half];
                                 const float* y = o[nb][4 * gr + 2 * half + 1];
                                 const float add = vbias[nb][gr][col];
+                                const float vref = __uint_as_float(
+                                    (254u << 23) - __float_as_uint(vinv[nb][gr][col]));
                                 *reinterpret_cast<float4*>(row + 4 * (u ^ sw)) =
                                     make_float4(fmaf(x[col] * 0x1p24f, vref, add),
                                                 fmaf(x[col + 2] * 0x1p20f, vref, add),
