@@ -97,7 +97,8 @@ typedef int32_t pkv_status;
 
 /* Supported shapes: head_dim in {64, 128}; page_size in {16, 32, 64, 128};
  * num_q_heads a multiple of num_kv_heads with a group of at most 16;
- * num_pages * num_kv_heads * page_size < 2^31. */
+ * num_pages * num_kv_heads * page_size < 2^31; attention: batch *
+ * ceil(max_pages * page_size / 64) < 2^31.  A length may be up to 2^31 - 1. */
 
 /*
  * kv_tag_check -- batched page-tag integrity check.

@@ -240,6 +240,14 @@ pkv_status check_common_kv(int32_t batch, int32_t num_kv_heads, int32_t head_dim
     return PKV_OK;
 }
 
+// The attention kernels count a batch's 64-token chunks in 32 bits.
+pkv_status check_chunks(int32_t batch, int32_t max_pages, int32_t page_size) {
+    const int64_t chunks = (static_cast<int64_t>(max_pages) * page_size - 1) / pkv::kChunkTokens + 1;
+    if (chunks * batch > INT32_MAX)
+        return fail(PKV_ERR_UNSUPPORTED, "batch * ceil(max_pages * page_size / 64) must be < 2^31");
+    return PKV_OK;
+}
+
 // The work split of one attention call (see paged_decode_attn_plan).
 struct AttnPlan {
     int kv_per_item;      // KV heads per work item the kernel uses
@@ -437,6 +445,8 @@ pkv_status attn_impl(const KvPools& pools, const uint16_t* q, const int32_t* pag
         return fail(PKV_ERR_INVALID_ARG, "num_ctas must be >= %d (got %d)", -pkv::kMaxCluster,
                     num_ctas);
     if (batch == 0) return PKV_OK;
+    st = check_chunks(batch, max_pages, page_size);
+    if (st != PKV_OK) return st;
     if (!q || !k_cache || !v_cache || !page_table || !seq_lens || !out || !lse ||
         (int4 && (!pools.k_params || !pools.v_params)))
         return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
@@ -582,6 +592,8 @@ pkv_status prefix_impl(const uint16_t* q, const uint8_t* k_cache, const uint8_t*
     if (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
         return fail(PKV_ERR_INVALID_ARG, "k_scale and v_scale must be finite and > 0");
     if (batch == 0) return PKV_OK;
+    st = check_chunks(batch, max_pages, page_size);
+    if (st != PKV_OK) return st;
     if (!q || !k_cache || !v_cache || !page_table || !seq_lens || !out || !lse)
         return fail(PKV_ERR_INVALID_ARG, "null pointer argument");
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 4) ||

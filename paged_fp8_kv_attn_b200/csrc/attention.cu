@@ -169,7 +169,8 @@ struct WindowGap {
 __device__ __forceinline__ WindowGap window_gap(int len, int window, int sinks) {
     const int lo = max(len - window, 0);                  // first token of the window
     const int w = lo / kChunkTokens;
-    const int s = (min(sinks, lo) + kChunkTokens - 1) / kChunkTokens;
+    const int st = min(sinks, lo);                        // sinks in front of it
+    const int s = st > 0 ? blocks_of(st, kChunkTokens) : 0;
     return {s, max(w - s, 0)};
 }
 
@@ -196,7 +197,7 @@ struct Walker {
 
     __device__ __forceinline__ int chunks_of(int32_t len) const {
         if (!(len >= 1 && static_cast<int64_t>(len) <= max_tokens)) return 0;
-        const int all = (len + kChunkTokens - 1) / kChunkTokens;
+        const int all = blocks_of(len, kChunkTokens);
         if constexpr (kWin) return all - window_gap(len, window, sinks).gap;
         return all;
     }
@@ -619,8 +620,8 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // (their page-table entry is then not used).
     auto hidden_box = [&](int len, int tok0) {
         if constexpr (kWin) {
-            const int lo = len - a.window;
-            return tok0 >= a.sinks && tok0 + box_toks <= lo;
+            const int lo = max(len - a.window, 0);
+            return tok0 >= a.sinks && tok0 <= lo - box_toks;
         } else {
             return false;
         }
@@ -639,7 +640,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             int count = 0;
             while (count < S && w2.next(s)) {
                 win.reset(a.page_table + static_cast<int64_t>(s.b) * a.max_pages);
-                const int npages = (s.L + P - 1) >> pshift;
+                const int npages = ((s.L - 1) >> pshift) + 1;
                 for (int ch = s.c0; ch < s.c1 && count < S; ++ch, ++count) {
                     const int rc = s.real(ch);
                     for (int i = 0; i < boxes; ++i) {
@@ -676,7 +677,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const int j0 = sg.real(sg.c0) * kChunkTokens >> pshift;
             if (w.row != row || w.base != j0) {
                 w.reset(row);
-                w.preload(j0, (sg.L + P - 1) >> pshift, lane);
+                w.preload(j0, ((sg.L - 1) >> pshift) + 1, lane);
             }
             return (a.abort != nullptr) ? static_cast<int>(a.abort[sg.b]) : 0;
         };
@@ -777,7 +778,7 @@ attn_partial_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                     static_cast<int64_t>(s.h) * kH * a.group) * kD;
                 if (lane * 64 < kH * a.group * kD) prefetch_l2(a.q + q0 + lane * 64);
             }
-            const int npages = (s.L + P - 1) >> pshift;
+            const int npages = ((s.L - 1) >> pshift) + 1;
             if constexpr (kInt4) {
                 if (direct) copy_segment(s, win, npages, it);
             }
@@ -1849,7 +1850,7 @@ attn_merge_kernel(const AttnArgs a) {
         for (int bb = tid; bb < a.batch; bb += kMergeThreads) {
             const int32_t len = a.seq_lens[bb];
             int nb = (len >= 1 && static_cast<int64_t>(len) <= max_tokens)
-                         ? (len + kChunkTokens - 1) / kChunkTokens
+                         ? blocks_of(len, kChunkTokens)
                          : 0;
             if (nb > 0 && a.window > 0) nb -= window_gap(len, a.window, a.sinks).gap;
             const int nc = nb;

@@ -163,6 +163,12 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
                  : "memory");
 }
+// Pages (chunks) of `size` tokens that `len` >= 1 tokens take.  (A length may be
+// 2^31 - 1, so size - 1 is not added to it.)
+__device__ __forceinline__ int32_t blocks_of(int32_t len, int32_t size) {
+    return (len - 1) / size + 1;
+}
+
 // Hint: bring the 128-byte line holding p into L2.
 __device__ __forceinline__ void prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));

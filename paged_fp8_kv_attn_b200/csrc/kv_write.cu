@@ -35,11 +35,11 @@ tag_check_kernel(const uint32_t* __restrict__ page_tags, int32_t num_pages,
     int bad = (L < 1 || static_cast<int64_t>(L) > static_cast<int64_t>(max_pages) * page_size);
     if (!bad) {
         // (window > 0: entries [skip, skip + gap) hold hidden tokens only)
-        int32_t used = (L + page_size - 1) / page_size, skip = used, gap = 0;
+        int32_t used = blocks_of(L, page_size), skip = used, gap = 0;
         if (window > 0) {
             const int32_t lo = L > window ? L - window : 0;
             const int32_t s = sinks < lo ? sinks : lo;
-            skip = (s + page_size - 1) / page_size;
+            skip = s > 0 ? blocks_of(s, page_size) : 0;
             gap = lo / page_size > skip ? lo / page_size - skip : 0;
             used -= gap;
         }
@@ -181,7 +181,7 @@ check_append_kernel(const uint32_t* __restrict__ page_tags, int32_t num_pages,
     if (!bad) {
         const int32_t pos = L - 1;
         slot = pos % page_size;
-        const int32_t used = (L + page_size - 1) / page_size;
+        const int32_t used = blocks_of(L, page_size);
         pid = row[pos / page_size];
         for (int j = j0; j < used; j += kFusedThreads) {
             const int32_t p = (j == j0) ? p_first : row[j];
@@ -262,7 +262,7 @@ expected_tags_kernel(const uint32_t* __restrict__ page_tags, int32_t num_pages,
     const int b = blockIdx.x;
     const int32_t L = seq_lens[b];
     if (L < 1 || static_cast<int64_t>(L) > static_cast<int64_t>(max_pages) * page_size) return;
-    const int32_t used = (L + page_size - 1) / page_size;
+    const int32_t used = blocks_of(L, page_size);
     const int64_t row = static_cast<int64_t>(b) * max_pages;
     for (int j = threadIdx.x; j < used; j += kTagOpThreads) {
         const int32_t p = page_table[row + j];

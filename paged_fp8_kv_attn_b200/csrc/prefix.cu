@@ -358,7 +358,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_cons
     // A tile's steps: its shared chunks (read through the reference row), then
     // for each member the tile finishes (chunk_begin = all its chunks) the
     // chunks after its shared ones (read through its own row).
-    auto n_chunks = [&](int bb) { return (a.seq_lens[bb] + kChunkTokens - 1) / kChunkTokens; };
+    auto n_chunks = [&](int bb) { return blocks_of(a.seq_lens[bb], kChunkTokens); };
     auto finished = [&](int bb) { return a.chunk_begin[bb] == n_chunks(bb); };
 
     if (lwarp == kPfxRowWarps) {
@@ -393,7 +393,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_cons
                     const int bb = b_first + k;
                     if (!finished(bb)) continue;
                     const int32_t* own = a.page_table + static_cast<int64_t>(bb) * a.max_pages;
-                    const int npages = (a.seq_lens[bb] + a.page_size - 1) / a.page_size;
+                    const int npages = blocks_of(a.seq_lens[bb], a.page_size);
                     for (int c = a.pshare[bb]; c < n_chunks(bb); ++c)
                         if (!load(own, c, p, npages)) break;
                 }
