@@ -205,6 +205,20 @@ def _match(name, t, shape):
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _i32(value, name):
+    """An int argument of the C call (ctypes would drop its bits past 32)."""
+    value = int(value)
+    if not -2**31 <= value < 2**31:
+        raise ValueError(f"{name} must fit in 32 bits, got {value}")
+    return value
+
+
+def _window(window, sinks):
+    """(window, sinks) of the C call: 2^31 - 1 stands for anything larger, since no
+    length passes it, and -1 for anything negative, which the call refuses."""
+    return tuple(min(max(int(x), -1), 2**31 - 1) for x in (window, sinks))
+
+
 def _tag_dtype(t, name):
     """The dtype of tags: one of _TAG_DTYPES."""
     return _need(t, _TAG_DTYPES, 1, name).dtype
@@ -257,8 +271,8 @@ def kv_tag_check_window(page_tags, page_table, expected_tags, seq_lens, page_siz
         _args(dev, (), ("num_aborted", num_aborted, i32, (1,)))
     _check("kv_tag_check_window", _load().kv_tag_check_window(
         _ptr(page_tags), page_tags.shape[0], _ptr(page_table), _ptr(expected_tags), MP,
-        _ptr(seq_lens), B, page_size, int(window), int(sinks), _ptr(abort_out), _ptr(num_aborted),
-        handle))
+        _ptr(seq_lens), B, _i32(page_size, "page_size"), *_window(window, sinks), _ptr(abort_out),
+        _ptr(num_aborted), handle))
 
 
 def kv_retag_pages(page_tags, pages, stream=None):
@@ -503,8 +517,9 @@ def kv_extend_tables(old_lens, new_lens, page_size, free_pages, num_free, page_t
         _args(dev, (), ("page_tags", page_tags, tag, (num_pages,)),
               ("expected_tags", expected_tags, tag, (B, MP)))
     _check("kv_extend_tables", _load().kv_extend_tables(
-        old_lens.data_ptr(), new_lens.data_ptr(), B, int(page_size), free_pages.data_ptr(), cap,
-        num_free.data_ptr(), num_free_out.data_ptr(), int(num_pages), page_table.data_ptr(), MP,
+        old_lens.data_ptr(), new_lens.data_ptr(), B, _i32(page_size, "page_size"),
+        free_pages.data_ptr(), cap, num_free.data_ptr(), num_free_out.data_ptr(),
+        _i32(num_pages, "num_pages"), page_table.data_ptr(), MP,
         _ptr(page_tags), _ptr(expected_tags), slot_map.data_ptr(), T, cu_tokens.data_ptr(),
         failed.data_ptr(), handle))
 
@@ -676,7 +691,7 @@ def _attn_call(name, pools, scales, shape, specs, q, page_table, seq_lens, sm_sc
     _check(name, getattr(_load(), name)(
         q.data_ptr(), *[t.data_ptr() for t in pools], *scales, page_table.data_ptr(), MP,
         seq_lens.data_ptr(), B, Hq, Hkv, D, P, NP, float(sm_scale), *window, _ptr(abort),
-        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ws, num_ctas, handle))
+        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ws, _i32(num_ctas, "num_ctas"), handle))
 
 
 def paged_decode_attn_int4(q, k_codes, k_params, v_codes, v_params, page_table, seq_lens, sm_scale,
@@ -695,7 +710,7 @@ def paged_decode_attn_fp8_window(q, k_cache, v_cache, k_scale, v_scale, page_tab
     shape = _need(k_cache, torch.uint8, 4, "k_cache").shape
     _attn_call("paged_decode_attn_fp8_window", (k_cache, v_cache), (float(k_scale), float(v_scale)),
                shape, (("v_cache", v_cache, torch.uint8, shape),), q, page_table, seq_lens,
-               sm_scale, (int(window), int(sinks)), out, lse, workspace, abort, num_ctas, stream)
+               sm_scale, _window(window, sinks), out, lse, workspace, abort, num_ctas, stream)
 
 
 def paged_decode_attn_bf16_window(q, k_cache, v_cache, page_table, seq_lens, sm_scale, window,
@@ -704,7 +719,7 @@ def paged_decode_attn_bf16_window(q, k_cache, v_cache, page_table, seq_lens, sm_
     shape = _need(k_cache, torch.bfloat16, 4, "k_cache").shape
     _attn_call("paged_decode_attn_bf16_window", (k_cache, v_cache), (), shape,
                (("v_cache", v_cache, torch.bfloat16, shape),), q, page_table, seq_lens,
-               sm_scale, (int(window), int(sinks)), out, lse, workspace, abort, num_ctas, stream)
+               sm_scale, _window(window, sinks), out, lse, workspace, abort, num_ctas, stream)
 
 
 def paged_decode_attn_int4_window(q, k_codes, k_params, v_codes, v_params, page_table, seq_lens,
@@ -714,7 +729,7 @@ def paged_decode_attn_int4_window(q, k_codes, k_params, v_codes, v_params, page_
     pools = (k_codes, k_params, v_codes, v_params)
     shape = _int4_shape(k_codes)
     _attn_call("paged_decode_attn_int4_window", pools, (), shape, _int4_specs(shape, *pools[1:]), q,
-               page_table, seq_lens, sm_scale, (int(window), int(sinks)), out, lse, workspace,
+               page_table, seq_lens, sm_scale, _window(window, sinks), out, lse, workspace,
                abort, num_ctas, stream)
 
 
