@@ -11,9 +11,14 @@ an output is sum w_t a_t + sum w_t m_t, and the kernel rounds
      w_t s_t over 8, the rounding is absolute: 2^-28 of the largest, or all of it;
  (2) scores: the products of a 16-dim step, exact, meet in a binary32 accumulator
      that may truncate; eight such steps and the sums around them, 16 units of 2^-24
-     of the sum of the parts' magnitudes, and 2^-22 of the exponential.  An error that
-     is common to a request's tokens divides out, so w_t moves out by it times (value -
-     out), independently;
+     of the sum of the parts' magnitudes, and 2^-22 of the exponential.  A code of an
+     even (odd) dim enters as a subnormal f16, up to 2^10 (2^6) times which the adder
+     may take for its magnitude: of 24 bits below the leading one of 2^10 (2^6) times
+     a step's largest |q|, the last is 2^-13 (2^-17) of that |q| at most.  The 8 bits
+     of a |q| reach below it only where it is less than 2^-6 (2^-10) of the largest,
+     so each such dim with a code loses up to one unit of 2^-13 (2^-17) of the head's
+     largest |q|, times the scale.  An error that is common to a request's tokens
+     divides out, so w_t moves out by it times (value - out), independently;
  (3) the V product's accumulator, once per tile of 16 tokens, truncating: 2^-23 of
      the sum of w_t |a_t| a time, all in one direction at worst; and the minima's sum,
      to nearest: 2^-24 of its magnitude, times the root of the number of sums;
@@ -58,8 +63,16 @@ def attend(q_bits, pools, table, lens, sm_scale, window=0, sinks=0, sums=None):
             o = w @ v
             # (2): the sums' magnitudes, the minima times the groups' query sums
             qs = np.abs(qh.reshape(G, K, GROUP).sum(-1))
-            size = sm * (np.abs(qh) @ np.abs(ka).T + qs @ np.abs(km[:, ::GROUP]).T)
+            size = abs(sm) * (np.abs(qh) @ np.abs(ka).T + qs @ np.abs(km[:, ::GROUP]).T)
             moved = 16 * U * (size + np.abs(s - s.max(-1, keepdims=True))) + 2.0 ** -22
+            top = np.abs(qh).max(-1, keepdims=True)
+            for parity, bits in ((0, 10), (1, 6)):
+                aq = np.abs(qh[:, parity::2])
+                small = (aq > 0) & (aq < 2.0 ** (bits - 16) * top)
+                # (a dim's |a| is at most 15 scales: the scale of its group where it has a code)
+                ks = np.repeat(np.abs(ref.bf16(pools.kp[pages, h, t % P])[..., 0]), GROUP // 2, -1)
+                moved = moved + abs(sm) * 2.0 ** (bits - 23) * top * \
+                    (small.astype(float) @ (ks * (ka[:, parity::2] != 0)).T)
             var = (w ** 2 @ va ** 2) * (2.0 ** -22 / 3)                     # (1)
             wm = (w * moved) ** 2
             var += wm @ v ** 2 - 2 * (wm @ v) * o + wm.sum(-1, keepdims=True) * o ** 2
