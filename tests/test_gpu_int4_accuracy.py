@@ -142,3 +142,28 @@ def test_long_request(cuda_device, G, H, D, P):
             tight.check(o, good[1], good)
         with pytest.raises(AssertionError):
             tight.check(good[0], l, good)
+
+
+@pytest.mark.parametrize("G,H,D,P", SHAPES)
+@pytest.mark.parametrize("at", [0, 70, 299])
+def test_the_only_weighted_token_comes_back(cuda_device, G, H, D, P, at):
+    """One token, first or late, with all the weight (the others have e^-50 of it at most):
+    its weight is 1 and rounds to nothing, so an output is its value to 2^-20 of its two
+    parts, and the half step of bf16."""
+    n = 300
+    p, q, table, lens = attention_case("int4", [n] * 3, G, H, D, P, seed=37)
+    q = ref.f32_bits_to_bf16(np.abs(ref.bf16(q)).astype(np.float32))
+    sm = D ** -0.5
+    sums = ref.bf16(q).sum(-1) * sm
+    for b in range(3):
+        set_key(p, table, b, at, (110.0 + 0.37 * b) / sums[b].min())
+    c = Cache(p)
+    _, a, m = p.rows("v", table[:, at // P], np.full(3, at % P))
+    want = np.repeat((a + m).reshape(3, H, 1, D), G, 2).reshape(3, H * G, D)
+    parts = np.repeat((np.abs(a) + np.abs(m)).reshape(3, H, 1, D), G, 2).reshape(3, H * G, D)
+    half = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(want), 2.0 ** -126))) - 8)
+    for ctas in (0, 1, 7, -2):
+        ws = c.workspace(3, H * G, ctas)
+        out, _ = c.attend(cuda(q), cuda(table), cuda(lens), sm, ws, num_ctas=ctas)
+        err = np.abs(values(out) - want)
+        assert (err <= half + 2.0 ** -20 * parts).all(), (ctas, (err / (half + 2.0 ** -20 * parts)).max())
