@@ -440,7 +440,9 @@ PKV_API pkv_status paged_decode_attn_plan(int32_t kv_dtype, int32_t batch, int32
  * same result up to rounding):
  *   0     the library chooses (cluster mode when the batch has no more
  *         (request, KV-head) items than the GPU holds resident CTAs, split-K
- *         over one wave otherwise);
+ *         over one wave otherwise; INT4 caches and windows: the shorter by an
+ *         estimate at the longest requests that max_pages allows, so that a
+ *         page table much wider than its requests may cost short batches time);
  *   N > 0 split-K over N CTAs;
  *   -C    cluster mode with clusters of C CTAs, 1 <= C <= 16
  *         (PKV_ERR_UNSUPPORTED if the device cannot run that cluster size).
@@ -543,8 +545,11 @@ PKV_API pkv_status paged_decode_attn_bf16(const uint16_t* q, const uint16_t* k_c
  * paged_decode_attn_int4 -- the same attention over an INT4 cache, whose
  * values s * code + m are formed while they are read (the K product and the V
  * product run over the codes; scales and minima are applied to scores and
- * weights).  k_codes / k_params and v_codes / v_params as in the conventions
- * above; everything else as for paged_decode_attn_fp8.  Workspace from
+ * weights).  The weights of the codes, softmax weight times scale, are f16
+ * relative to a power of two that each query head keeps per group of 64 dims;
+ * everything else is binary32.  k_codes / k_params and v_codes / v_params as in the conventions
+ * above; everything else as for paged_decode_attn_fp8 (num_ctas = 0: the choice
+ * for INT4 caches).  Workspace from
  * paged_decode_attn_workspace_size(PKV_KV_INT4, ...).
  */
 PKV_API pkv_status paged_decode_attn_int4(const uint16_t* q, const uint8_t* k_codes,

@@ -279,10 +279,11 @@ bool modelled_split(int kv, int32_t window) { return kv == PKV_KV_INT4 || window
 // Requests of one batch differ in length, which split-K evens out and whole items
 // do not: a cluster's chunks count 25% more, but for a window shorter than the
 // table's longest request, which makes most of them equal (96 requests of up to
-// 8,190 tokens, 64 dims: clusters of one 116, split-K 77).
-// Measured, this choice / the item-count rule: INT4 64 x 8,192 tokens 135 / 147
-// (split-K), 2 x 131,072 81 / 160 (split-K), 128 x 16 15.4 / 25.9 (clusters of
-// one), FP8 window of 400 over 128 x 600 34.6 / 41.5 (clusters of one).
+// 8,190 tokens, 64 dims: clusters of one 114, split-K 79; that one batch set the 25%).
+// Measured cold, this choice / the item-count rule: INT4 64 x 8,192 tokens 137 / 150
+// (split-K), 2 x 131,072 82 / 128 (split-K), 128 x 16 22 / 32 (clusters of one; with
+// a table much wider than the requests split-K, 25), FP8 window of 400 over 128 x 600
+// 37 / 48 (clusters of one), INT4 window of 16,384 over 8 x 65,536 58 / 57 (split-K).
 pkv_status model_split(int kv, int head_dim, int group, bool window, int page_size, int32_t batch,
                        int64_t items, int wide, int64_t chunks, int grid, int* kv_per_item,
                        int* cluster, int* nclusters) {
@@ -355,8 +356,8 @@ pkv_status plan_attention(int kv, int32_t batch, int32_t num_kv_heads, int32_t g
         const int64_t max_units =
             static_cast<int64_t>(batch) * (num_kv_heads / kv_per_item) * chunks_per_seq;
         int64_t cap = std::max<int64_t>(info->sms, (max_units + 7) / 8);
-        // INT4 and windows: nor fewer CTAs than items (short requests; measured with
-        // 128 x 16 tokens, 512 items: 18.3 us on 444 CTAs, 25.9 on 148)
+        // INT4 and windows: nor fewer CTAs than items (short requests; measured cold with
+        // 128 x 16 tokens, 512 items: 25.0 us on 444 CTAs, 32.0 on 148)
         if (modelled_split(kv, window))
             cap = std::max<int64_t>(cap, static_cast<int64_t>(batch) * (num_kv_heads / kv_per_item));
         if (cap < grid) grid = static_cast<int>(cap);

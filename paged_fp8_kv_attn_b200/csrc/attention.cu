@@ -45,8 +45,10 @@
 //    q . k = sum_groups s (q . code) + m sum(q), and the weighted sum of V is
 //    sum (w s) code + sum w m.  The products run over the codes as they lie in
 //    shared memory (one AND makes an operand pair); scales and minima are applied
-//    per token.  Bound by issue and the ALU pipe, not by memory: 64 x 8,192 tokens
-//    of 8 heads x 128 dims take 133 us where their 606 MB take 92.
+//    per token.  Not bound by memory: 64 x 8,192 tokens of 8 heads x 128 dims take
+//    137 us (cold, with the launch) where their 606 MB take 92, with half of DRAM's
+//    rate, half of the issue slots and half of the ALU pipe in use.  Small INT4 pages
+//    are copied by all of the producer's lanes instead of TMA boxes.
 //  * Window: units are the chunks that hold a visible token; the ones at its
 //    edges mask scores and V rows as the last chunk of a request does.
 #include "device.cuh"
@@ -60,8 +62,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;
 // INT4: scores may pass the running maximum by 12, which most never do after a segment's
-// first tokens (against 8: 64 x 8,192 tokens 131.0 us of 132.3, groups of 16 heads 78.8 of
-// 80.9).  Weights times scales are held in f16 relative to a power of two per head and
+// first tokens (against 8: 64 x 8,192 tokens 136.5 us of 137.1, groups of 16 heads 89.4 of
+// 91.3).  Weights times scales are held in f16 relative to a power of two per head and
 // group that puts the largest so far at 8 to 16 when it is set, and again when one passes
 // kInt4WeightMax: twelve octaves for the scores' rise, and 2^-28 of the largest at the
 // small end.
@@ -90,9 +92,9 @@ struct AttnCfg {
     // INT4 pages of at most this many tokens are copied 16 bytes a lane by the
     // whole producer warp; larger ones as TMA boxes.  A box costs its one issuing
     // lane the same whatever its size, so it pays from 4 KB of codes on.  Measured
-    // (444 CTAs, TMA / copies): D = 128, 64 x 8,192 tokens, pages of 64: 133 / 149 us,
-    // of 32: 138 / 153, of 16: 169 / 155; D = 64, 96 ragged requests, pages of 64:
-    // 73 / 75, of 32: 83 / 75, of 16: 112 / 77.
+    // (444 CTAs, cold, TMA / copies): D = 128, 64 x 8,192 tokens, pages of 64: 136 / 158
+    // us, of 32: 141 / 158, of 16: 173 / 158; D = 64, 96 ragged requests, pages of 64:
+    // 75 / 76, of 32: 83 / 77, of 16: 111 / 79.
     static constexpr int kDirectPage = kInt4 ? int4_direct_page(kD) : 0;
     static constexpr int kStageBytes = (2 * (kTileBytes + kParTileBytes) + 1023) / 1024 * 1024;
     // Pipeline depth and resident CTAs per SM, chosen by measurement on B200:

@@ -21,7 +21,7 @@ constexpr int kFlight = kOne ? 4 : 1;
 
 // The calling warp's part of a call: blocks [0, total) of its tokens' rows.
 // kOne: a single token, whose slot is loaded and resolved once (8,192 tokens of
-// 8 x 128, INT4: write 16.6 us, read 9.4; block by block 18.8 and 11.7).
+// 8 x 128, INT4: write 16.6 us, read 9.6; block by block 18.8 and 11.7).
 template <int kD, bool kOne>
 struct SlotWork {
     const SlotArgs& a;
