@@ -1200,6 +1200,8 @@ pkv_status paged_decode_attn_plan(int32_t kv_dtype, int32_t batch, int32_t num_q
     if (group > 16) return fail(PKV_ERR_UNSUPPORTED, "GQA group %d > 16 not supported", group);
     if (num_ctas < -pkv::kMaxCluster)
         return fail(PKV_ERR_INVALID_ARG, "num_ctas must be >= %d", -pkv::kMaxCluster);
+    st = check_chunks(batch, max_pages, page_size);
+    if (st != PKV_OK) return st;
     AttnPlan plan;
     st = plan_attention(kv_dtype, batch, num_kv_heads, group, head_dim, max_pages, page_size, 0, 0,
                         num_ctas, &plan);

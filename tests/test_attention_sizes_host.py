@@ -34,3 +34,12 @@ def test_chunk_counts_beyond_32_bits(lib, kind):
     assert call(1, 2**31 - 1, 128) == 3
     assert call(4, 2**31 - 1, 16) == 3
     assert call(3, 2**31 - 1, 16) == 2
+
+
+@pytest.mark.parametrize("kind", [pkv.PKV_KV_FP8, pkv.PKV_KV_BF16, pkv.PKV_KV_INT4])
+def test_plan_refuses_what_the_call_refuses(lib, kind):
+    out = [ctypes.c_int32(0) for _ in range(3)]
+    plan = lambda batch, pages: lib.paged_decode_attn_plan(  # noqa: E731
+        kind, batch, 8, 4, 128, pages, 128, 0, *[ctypes.byref(o) for o in out])
+    assert plan(64, 1 << 24) == 3 and b"2^31" in lib.pkv_last_error()
+    assert plan(1, 2**31 - 1) == 3
